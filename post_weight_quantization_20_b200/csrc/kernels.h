@@ -1,6 +1,7 @@
 // Internal host-side entry points shared between the library's translation units.
 #pragma once
 #include "common.cuh"
+#include "gptq_cache.h"
 
 namespace gptq {
 
@@ -60,5 +61,25 @@ gptq_status dequant_matmul_run(cudaStream_t st, const void* X, int xdt, int M, i
 // pack.cu
 gptq_status pack_run(cudaStream_t st, const uint8_t* codes, int64_t R, int64_t C, int bits,
                      uint32_t* packed);
+
+// mx.cu: microscaled 4-bit rows; whether the launch grid holds rows x cols
+bool mx_grid_fits(int64_t rows, int64_t cols);
+gptq_status mx_quantize_run(cudaStream_t st, const void* X, int dt, int64_t rows, int cols,
+                            int64_t ldx, uint32_t* codes, uint8_t* scales, int32_t* status);
+gptq_status mx_dequantize_run(cudaStream_t st, const uint32_t* codes, const uint8_t* scales,
+                              int64_t rows, int cols, void* Y, int dt, int64_t ldy);
+
+// mx_matmul.cu: Y = X W^T of two microscaled matrices on tcgen05
+gptq_status mx_matmul_run(cudaStream_t st, const uint32_t* xc, const uint8_t* xs, int M,
+                          const uint32_t* wc, const uint8_t* ws, int R, int C, void* Y, int dt,
+                          int64_t ldy, int32_t* status);
+
+// kv_cache.cu: words of codes and groups of one token and head (false: not supported), and
+// the two passes over the rows of a call (write: into the cache)
+bool cache_shape(const gptq_cache_config& cfg, int64_t dim, int& words, int& groups);
+gptq_status cache_run(cudaStream_t st, bool write, const void* K, const void* V, int dtype,
+                      int64_t tokens, int64_t k_ld_token, int64_t k_ld_head, int64_t v_ld_token,
+                      int64_t v_ld_head, const gptq_cache_config& cfg, const gptq_cache& cache,
+                      const gptq_cache_rows& rows, int32_t* status);
 
 }  // namespace gptq

@@ -23,6 +23,7 @@
 
 #include "common.cuh"
 #include "gemm_f32.cuh"
+#include "grid.cuh"
 #include "kernels.h"
 
 namespace gptq {
@@ -70,21 +71,6 @@ size_t quantize_ws_bytes(int64_t R, int64_t C, const gptq_config&) {
   return align256(size_t(R) * C * 4) + 2 * align256(size_t(R) * SW_LDERR * 4) +
          align256(size_t(R) * C) + align256(size_t(tiles) * C * 4) +
          2 * align256(size_t(C) * C * 4) + 256;
-}
-
-// Grid of a set of values with range [lo, hi] (lo <= 0 <= hi), all in IEEE fp32.
-__device__ __forceinline__ void grid_params(float lo, float hi, float maxq, int sym, float& s,
-                                            float& z) {
-  if (sym) {
-    float m = fmaxf(-lo, hi);
-    if (m == 0.f) m = 1.f;
-    s = __fdiv_rn(__fsub_rn(m, -m), maxq);
-    z = (maxq + 1.f) * 0.5f;
-  } else {
-    if (lo == 0.f && hi == 0.f) { lo = -1.f; hi = 1.f; }
-    s = __fdiv_rn(__fsub_rn(hi, lo), maxq);
-    z = rintf(__fdiv_rn(-lo, s));
-  }
 }
 
 // Wk[r][j] = W[r][perm[j]] as fp32.
