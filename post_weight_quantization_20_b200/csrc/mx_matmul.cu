@@ -2,13 +2,20 @@
 // tensor cores: tcgen05.mma kind::mxf4 multiplies the codes and applies both sides' scales
 // (one per 32 columns) itself, so nothing is dequantised.
 //
-// The MMA's M side is W (128 rows of the layer per tile) and its N side the tokens, so that
-// one token costs an N = 16 tile and a thread of the epilogue holds one layer row, whose
-// neighbours in a warp are neighbours in Y's rows.  K runs in stages of 256 columns: 128
-// bytes of codes per row (TMA, 128-byte swizzle) and two 512-byte scale tiles per 128 rows.
-// The scales reach TMEM with tcgen05.cp; every stage of the ring has TMEM columns of its own
-// for them, so they are overwritten only after the MMAs that read them have released the
-// stage.  Per CTA: warp 0 producer, warp 1 TMEM and MMA, warps 2-5 epilogue.
+// The MMA's M side is W and its N side the tokens, so that few tokens cost a narrow tile and
+// a thread of the epilogue holds one layer row, whose neighbours in a warp are neighbours in
+// Y's rows.  K runs in boxes of 256 columns: 128 bytes of codes per row (TMA, 128-byte
+// swizzle) and two 512-byte scale tiles per 128 rows.  The scales reach TMEM with tcgen05.cp;
+// every stage of the ring has TMEM columns of its own for them, so they are overwritten only
+// after the MMAs that read them have released the stage.
+//
+// Two kernels:
+//  k_mx_few    128 layer rows x up to 128 tokens per CTA, K split over the CTAs of a cluster,
+//              whose partial sums meet in distributed shared memory in a fixed order: few
+//              tokens, where the weights' bytes are the work and row tiles alone would leave
+//              SMs idle.
+//  k_mx_pair   256 layer rows x up to 256 tokens per CTA pair (cta_group::2), persistent:
+//              many tokens.
 // Every mbarrier wait is bounded; a wait that gives up sets GPTQ_ERR_TIMEOUT and the CTA
 // drains its own copies and MMAs before it frees TMEM and exits.
 #include <algorithm>
@@ -20,24 +27,8 @@
 namespace gptq {
 namespace {
 
-constexpr int TM = 128;                 // layer rows per tile
-constexpr int KB = 128;                 // bytes of codes per row and stage: 256 columns
-constexpr int A_BYTES = TM * KB;
-constexpr int THREADS = 192;
-
-template <int BN>
-struct Cfg {
-  static constexpr int NB = (BN + 127) / 128;                 // scale tiles of the token side
-  static constexpr int B_BYTES = BN * KB;
-  static constexpr int S_BYTES = (1 + NB) * 1024;             // both scale tiles of each 128 rows
-  static constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;   // a multiple of 1024
-  static constexpr int STAGES = 200 * 1024 / STAGE < 6 ? 200 * 1024 / STAGE : 6;
-  static constexpr int SF_COLS = 8 * (1 + NB);                // TMEM columns of a stage's scales
-  static constexpr int COLS = BN + STAGES * SF_COLS;
-  static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
-  static_assert(COLS <= 512, "TMEM");
-};
+constexpr int KB = 128;                 // bytes of codes per row and box: 256 columns
+constexpr int A_BOX = 128 * KB;
 
 struct Prob {
   const uint8_t* xs;
@@ -46,15 +37,45 @@ struct Prob {
   int64_t ldy;
   int M, R;          // tokens, layer rows
   int steps;         // MMAs along K: 64 columns each
-  int ct;            // scale tiles along K
+  int ct;            // scale tiles along K: 128 columns each
+  int boxes;         // boxes along K: 256 columns each
   uint32_t wait_limit;
+  // k_mx_pair only
+  int bn;            // tokens of a tile, a multiple of 32
+  int nb;            // scale tiles that a token tile touches
+  int ntr, ntt;      // tiles along the layer rows and the tokens
+};
+
+// sf_id of both operands for the odd 64-column half of a scale tile: bytes 2 and 3
+constexpr uint32_t ODD_HALF = (2u << 4) | (2u << 29);
+
+// idesc: 4-bit codes on both sides, K-major, byte scales 2^(e-127)
+constexpr uint32_t idesc_of(int m, int n) {
+  return (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (1u << 23) | (uint32_t(m >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ few tokens
+constexpr int FEW_THREADS = 192;        // warp 0 producer, warp 1 TMEM and MMA, 2-5 epilogue
+
+template <int BN>
+struct Few {
+  static constexpr int SUB = BN <= 64 ? 2 : 1;                // boxes of a stage
+  static constexpr int B_BOX = BN * KB;
+  static constexpr int S_BOX = 1024;                          // scales of 128 rows and a box
+  static constexpr int STAGE = SUB * (A_BOX + B_BOX + 2 * S_BOX);
+  static constexpr int STAGES = 200 * 1024 / STAGE < 6 ? 200 * 1024 / STAGE : 6;
+  static constexpr int SF_COLS = SUB * 16;                    // TMEM columns of a stage's scales
+  static constexpr int COLS = BN + STAGES * SF_COLS;
+  static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+  static_assert(COLS <= 512 && BN * 512 <= STAGES * STAGE, "TMEM, partial sums");
 };
 
 template <int BN, typename T>
-__global__ void __launch_bounds__(THREADS, 1)
-k_mx_matmul(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-            Prob p, uint32_t idesc, int32_t* status) {
-  using C = Cfg<BN>;
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+         Prob p, int32_t* status) {
+  using C = Few<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -65,9 +86,12 @@ k_mx_matmul(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = blockIdx.x * TM, n0 = blockIdx.y * BN;
-  const int nk = (p.steps + 3) >> 2;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int split = int(tc::cluster_rank()), splits = int(tc::cluster_size());
+  const int rt = blockIdx.x / splits;
+  const int r0 = rt * 128, n0 = blockIdx.y * BN;
+  const int b0 = int(int64_t(p.boxes) * split / splits);
+  const int b1 = int(int64_t(p.boxes) * (split + 1) / splits);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
@@ -90,84 +114,121 @@ k_mx_matmul(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
   int64_t issued = 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      // scale tiles of the token side that exist: a 256-token tile may hold one only
-      const int nbt = min(C::NB, (p.M + 127) / 128 - n0 / 128);
-      for (int k = 0; k < nk; ++k) {
-        if (!tc::mbar_wait(empty + stage, phase ^ 1u, abort_flag, p.wait_limit)) break;
-        uint8_t* a = smem + stage * C::STAGE;
-        uint8_t* s = a + A_BYTES + C::B_BYTES;
-        const uint32_t sb = uint32_t(min(2, p.ct - 2 * k)) * 512;
-        tc::mbar_expect_tx(full + stage, uint32_t(A_BYTES + C::B_BYTES) + sb * (1 + nbt));
-        tc::tma_load_2d(a, &wmap, k * KB, r0, full + stage);
-        tc::tma_load_2d(a + A_BYTES, &xmap, k * KB, n0, full + stage);
-        tc::bulk_load(s, p.ws + (int64_t(blockIdx.x) * p.ct + 2 * k) * 512, sb, full + stage);
-        for (int j = 0; j < nbt; ++j)
-          tc::bulk_load(s + 1024 * (1 + j),
-                        p.xs + (int64_t(n0 / 128 + j) * p.ct + 2 * k) * 512, sb, full + stage);
-        ++issued;
-        if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int b = b0; b < b1; b += C::SUB) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(empty + stage, phase ^ 1u, abort_flag, p.wait_limit)))
+        break;
+      const int nbx = min(C::SUB, b1 - b);
+      uint8_t* a = smem + stage * C::STAGE;
+      uint8_t* x = a + C::SUB * A_BOX;
+      uint8_t* s = x + C::SUB * C::B_BOX;
+      const uint32_t sb = uint32_t(min(2 * nbx, p.ct - 2 * b)) * 512;
+      if (tc::elect_one()) {
+        tc::mbar_expect_tx(full + stage, uint32_t(nbx * (A_BOX + C::B_BOX)) + 2 * sb);
+        for (int j = 0; j < nbx; ++j)
+          tc::tma_load_2d(a + j * A_BOX, &wmap, (b + j) * KB, r0, full + stage);
+        tc::bulk_load(s, p.ws + (int64_t(rt) * p.ct + 2 * b) * 512, sb, full + stage);
+        for (int j = 0; j < nbx; ++j)
+          tc::tma_load_2d(x + j * C::B_BOX, &xmap, (b + j) * KB, n0, full + stage);
+        tc::bulk_load(s + C::SUB * C::S_BOX, p.xs + (int64_t(n0 / 128) * p.ct + 2 * b) * 512, sb,
+                      full + stage);
       }
+      __syncwarp();
+      ++issued;
+      if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int k = 0; k < nk; ++k) {
-        if (!tc::mbar_wait(full + stage, phase, abort_flag, p.wait_limit)) { ok = false; break; }
-        tc::fence_after_sync();
-        const uint8_t* a = smem + stage * C::STAGE;
-        const uint8_t* b = a + A_BYTES;
-        const uint8_t* s = b + C::B_BYTES;
-        const uint32_t sfa = tmem_base + uint32_t(BN + stage * C::SF_COLS);
-        const uint32_t sfb = sfa + 8;
-        const int tiles = min(2, p.ct - 2 * k);
-        for (int t = 0; t < tiles; ++t) {
-          tc::copy_scales(sfa + 4 * t, tc::smem_desc_rows16(s + 512 * t));
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    constexpr uint32_t idesc = idesc_of(128, BN);
+    const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
+    const uint64_t sdesc0 = tc::smem_desc_rows16(smem + C::SUB * (A_BOX + C::B_BOX));
+    // a token tile of 32 or 64 starts inside its scale tile, 32 rows to a TMEM column
+    const uint32_t first = uint32_t((n0 & 127) >> 5);
+    for (int b = b0; b < b1; b += C::SUB) {
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(full + stage, phase, abort_flag, p.wait_limit));
+      if (!ok) break;
+      tc::fence_after_sync();
+      // descriptors count in 16 bytes
+      const uint64_t ad = adesc0 + uint32_t(stage) * (C::STAGE >> 4);
+      const uint64_t xd = ad + (C::SUB * A_BOX >> 4);
+      const uint64_t sd = sdesc0 + uint32_t(stage) * (C::STAGE >> 4);
+      const uint32_t sfa = tmem_base + uint32_t(BN + stage * C::SF_COLS);
+      const uint32_t sfb = sfa + 8 * C::SUB;
+      const int tiles = min(2 * C::SUB, min(2 * (b1 - b), p.ct - 2 * b));
+      const int todo = min(4 * C::SUB, min(4 * (b1 - b), p.steps - 4 * b));
+      if (tc::elect_one()) {
 #pragma unroll
-          for (int j = 0; j < C::NB; ++j)
-            tc::copy_scales(sfb + 4 * C::NB * t + 4 * j,
-                            tc::smem_desc_rows16(s + 1024 * (1 + j) + 512 * t));
-        }
-        const int todo = min(4, p.steps - 4 * k);
-        // a token tile of 32 or 64 starts inside its scale tile, 32 rows to a TMEM column
-        const uint32_t sfb0 = sfb + uint32_t((n0 & 127) >> 5);
-        for (int kk = 0; kk < todo; ++kk)
-          tc::mma_mxf4(tmem_base, tc::smem_desc_sw128(a + kk * 32, 16, 1024),
-                       tc::smem_desc_sw128(b + kk * 32, 16, 1024),
-                       idesc | ((kk & 1) ? (2u << 4) | (2u << 29) : 0u), sfa + 4 * (kk >> 1),
-                       sfb0 + 4 * C::NB * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
+        for (int t = 0; t < 2 * C::SUB; ++t)
+          if (t < tiles) {
+            tc::copy_scales(sfa + 4 * t, sd + 32 * t);
+            tc::copy_scales(sfb + 4 * t, sd + (C::SUB * C::S_BOX >> 4) + 32 * t);
+          }
+#pragma unroll
+        for (int kk = 0; kk < 4 * C::SUB; ++kk)
+          if (kk < todo)
+            tc::mma_mxf4(tmem_base, ad + (kk >> 2) * (A_BOX >> 4) + (kk & 3) * 2,
+                         xd + (kk >> 2) * (C::B_BOX >> 4) + (kk & 3) * 2,
+                         idesc | ((kk & 1) ? ODD_HALF : 0u), sfa + 4 * (kk >> 1),
+                         sfb + first + 4 * (kk >> 1), (b > b0 || kk > 0) ? 1u : 0u);
         tc::mma_commit(empty + stage);
-        if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
+        if (b + C::SUB >= b1) tc::mma_commit(acc_full);
       }
-      if (ok) tc::mma_commit(acc_full);
+      __syncwarp();
+      if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
     }
   } else {
+    // lane base + lane is a layer row, a TMEM column a token
     const int lane_base = (warp & 3) * 32;
     const int row = r0 + lane_base + lane;
     if (tc::mbar_wait(acc_full, 0, abort_flag, p.wait_limit)) {
       tc::fence_after_sync();
-      for (int c = 0; c < BN; c += 16) {
+      float* part = reinterpret_cast<float*>(smem);      // [token][128 rows]; the ring is empty
+      const int live = min(BN, p.M - n0);
+      for (int c = 0; c < live; c += 16) {
         uint32_t v[16];
         tc::tmem_ld_32x16(tmem_base + (uint32_t(lane_base) << 16) + uint32_t(c), v);
         tc::tmem_ld_wait();
-        T* y = static_cast<T*>(p.Y) + int64_t(n0 + c) * p.ldy + row;
+        if (splits == 1) {
+          T* y = static_cast<T*>(p.Y) + int64_t(n0 + c) * p.ldy + row;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (row < p.R && n0 + c + i < p.M) y[i * p.ldy] = from_f32<T>(__uint_as_float(v[i]));
+          for (int i = 0; i < 16; ++i)
+            if (row < p.R && c + i < live) y[i * p.ldy] = from_f32<T>(__uint_as_float(v[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[(c + i) * 128 + lane_base + lane] = __uint_as_float(v[i]);
+        }
       }
     }
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (splits > 1) {
+    // every CTA of the cluster sums its share of the tokens, the splits in order
+    tc::cluster_sync();
+    if (warp >= 2) {
+      const int i = (warp & 3) * 32 + lane, row = r0 + i;
+      const int live = min(BN, p.M - n0);
+      for (int t = split; t < live; t += splits) {
+        float v = 0.f;
+        for (int q = 0; q < splits; ++q)
+          v += tc::ld_cluster_f32(tc::cluster_addr(smem + (t * 128 + i) * 4, uint32_t(q)));
+        if (row < p.R) static_cast<T*>(p.Y)[int64_t(n0 + t) * p.ldy + row] = from_f32<T>(v);
+      }
+    }
+    __syncwarp();
+    tc::cluster_sync();                // no CTA leaves while its partial sums are read
+  }
   if (*abort_flag) {
     if (warp == 0 && lane == 0) tc::drain_tma_ring(full, C::STAGES, issued);
-    if (warp == 1 && lane == 0) {
-      tc::mma_commit(drain);
-      tc::mbar_drain(drain, 0);
+    if (warp == 1) {                 // by the lane that issued the MMAs
+      if (tc::elect_one()) {
+        tc::mma_commit(drain);
+        tc::mbar_drain(drain, 0);
+      }
+      __syncwarp();
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -179,6 +240,241 @@ k_mx_matmul(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CU
   }
 }
 
+// ------------------------------------------------------------------ many tokens
+// A pair of CTAs computes 256 layer rows x bn tokens: rank r loads layer rows r0 + 128 r ..
+// and tokens n0 + bn/2 r .. (its halves of the operands), the scales of its layer rows and of
+// all of the tile's tokens; rank 0 issues the MMAs.  The accumulator rows r0 + 128 r .. land
+// in rank r's TMEM.  8 epilogue warps per CTA take the whole tile into registers and release
+// the accumulator before they convert and store, so that the next tile's MMAs run meanwhile
+// (two accumulators of 256 tokens and the scales do not fit the 512 TMEM columns).
+namespace pair {
+
+constexpr int STAGES = 6;
+constexpr int BN = 256;                           // widest token tile
+constexpr int NB = 3;                             // scale tiles a token tile touches at most
+constexpr int B_BYTES = BN / 2 * KB;              // 16 KB
+constexpr int STAGE = A_BOX + B_BYTES + 1024 * (1 + NB);
+constexpr int SF_COLS = 8 * (1 + NB);
+constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+constexpr int THREADS = 320;
+constexpr int GROUP = 8;                          // token tiles per group of the tile order
+static_assert(BN + STAGES * SF_COLS <= 512, "TMEM");
+
+// t-th tile: groups of GROUP token tiles, row tile by row tile inside a group, so that the
+// tiles in flight together share operand rows in L2
+__device__ __forceinline__ void tile_of(const Prob& p, int t, int& r0, int& n0) {
+  const int per = GROUP * p.ntr;
+  const int g = t / per, q = t - g * per;
+  const int w = min(GROUP, p.ntt - g * GROUP);
+  r0 = q / w * 256;
+  n0 = (g * GROUP + q % w) * p.bn;
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+          const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
+          Prob p, uint32_t idesc, int32_t* status) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* drain = acc_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* issued_slot = tmem_slot + 2;          // the partner's fill count (abort path)
+
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_rank();
+  const int pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int tiles = p.ntr * p.ntt;
+  // bytes of one fill, both CTAs' loads (boxes past the tensors' ends count in full)
+  const uint32_t fill = 2 * uint32_t(A_BOX + p.bn / 2 * KB + 1024 * (1 + p.nb));
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      tc::mbar_init(full + i, 1);
+      tc::mbar_init(empty + i, 1);
+    }
+    tc::mbar_init(acc_full, 1);
+    tc::mbar_init(acc_empty, 16);                 // 8 epilogue warps of each CTA
+    tc::mbar_init(drain, 1);
+    *abort_flag = 0;
+    *issued_slot = 0;
+    tc::fence_barrier_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc_pair(tmem_slot, 512);
+    tc::tmem_relinquish_pair();
+  }
+  tc::fence_before_sync();
+  tc::cluster_sync();                             // both CTAs' barriers and TMEM ready
+  tc::fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t peer_flag = tc::cluster_addr(const_cast<int*>(abort_flag), rank ^ 1u);
+  int64_t issued = 0;
+
+  const auto load = [&](int stage, int b, int r0, int n0) {
+    uint8_t* a = smem + stage * STAGE;
+    uint8_t* x = a + A_BOX;
+    uint8_t* s = x + B_BYTES;
+    if (rank == 0) tc::mbar_expect_tx(full + stage, fill);
+    const uint32_t cbar = tc::cluster_addr(full + stage, 0);
+    tc::tma_load_2d_pair(a, &wmap, b * KB, r0 + 128 * int(rank), cbar);
+    tc::tma_load_2d_pair(x, &xmap, b * KB, n0 + p.bn / 2 * int(rank), cbar);
+    tc::tma_load_2d_pair(s, &wsmap, b * 256, r0 / 128 + int(rank), cbar);
+    tc::tma_load_2d_pair(s + 1024, &xsmap, b * 256, n0 / 128, cbar);
+  };
+
+  const auto wait = [&](uint64_t* bar, uint32_t parity, bool cluster_scope = false) {
+    return __all_sync(0xffffffffu, tc::mbar_wait_pair(bar, parity, abort_flag, peer_flag, p.wait_limit,
+                                                      cluster_scope));
+  };
+
+  if (warp == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = pair_id; t < tiles && ok; t += n_pairs) {
+      int r0, n0;
+      tile_of(p, t, r0, n0);
+      for (int b = 0; b < p.boxes; ++b) {
+        if (!wait(empty + stage, phase ^ 1u)) { ok = false; break; }
+        if (tc::elect_one()) load(stage, b, r0, n0);
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+    }
+    // every fill consumed: the MMAs' last arrivals on this CTA's empty barriers have landed
+    // before the CTA can exit
+    if (ok)
+      for (int st = 0; st < STAGES; ++st) {
+        const int64_t n = issued / STAGES + (st < issued % STAGES ? 1 : 0);
+        if (n > 0 && !wait(empty + st, uint32_t((n - 1) & 1))) break;
+      }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      int stage = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
+      const uint64_t sdesc0 = tc::smem_desc_rows16(smem + A_BOX + B_BYTES);
+      for (int t = pair_id; t < tiles && ok; t += n_pairs) {
+        int r0, n0;
+        tile_of(p, t, r0, n0);
+        const uint32_t first = uint32_t((n0 & 127) >> 5);
+        if (!wait(acc_empty, acc_phase ^ 1u, true)) break;
+        acc_phase ^= 1u;
+        tc::fence_after_sync();
+        for (int b = 0; b < p.boxes; ++b) {
+          if (!wait(full + stage, phase)) { ok = false; break; }
+          tc::fence_after_sync();
+          // descriptors count in 16 bytes
+          const uint64_t ad = adesc0 + uint32_t(stage) * (STAGE >> 4);
+          const uint64_t xd = ad + (A_BOX >> 4);
+          const uint64_t sd = sdesc0 + uint32_t(stage) * (STAGE >> 4);
+          const uint32_t sfa = tmem_base + uint32_t(BN + stage * SF_COLS);
+          const uint32_t sfb = sfa + 8, half = 4 * uint32_t(p.nb);
+          const int todo = p.steps - 4 * b;
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tc::copy_scales_pair(sfa + 4 * h, sd + 32 * h);
+#pragma unroll
+              for (int j = 0; j < NB; ++j)
+                if (j < p.nb) tc::copy_scales_pair(sfb + half * h + 4 * j, sd + 64 * (1 + j) + 32 * h);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < todo)
+                tc::mma_mxf4_pair(tmem_base, ad + 2 * kk, xd + 2 * kk,
+                                  idesc | ((kk & 1) ? ODD_HALF : 0u), sfa + 4 * (kk >> 1),
+                                  sfb + first + half * (kk >> 1), (b > 0 || kk > 0) ? 1u : 0u);
+            tc::mma_commit_pair(empty + stage, 0x3);
+            if (b + 1 == p.boxes) tc::mma_commit_pair(acc_full, 0x3);
+          }
+          __syncwarp();
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+    }
+  } else {
+    const int lane_base = (warp & 3) * 32;
+    const int c0 = ((warp - 2) >> 2) * 128;       // this warp's tokens of the tile
+    const uint32_t acc_empty0 = tc::cluster_addr(acc_empty, 0);
+    uint32_t acc_phase = 0;
+    for (int t = pair_id; t < tiles; t += n_pairs) {
+      int r0, n0;
+      tile_of(p, t, r0, n0);
+      if (!tc::mbar_wait_pair(acc_full, acc_phase, abort_flag, peer_flag, p.wait_limit)) break;
+      acc_phase ^= 1u;
+      tc::fence_after_sync();
+      uint32_t v[4][32];
+      const uint32_t at = tmem_base + (uint32_t(lane_base) << 16) + uint32_t(c0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c0 + 32 * c < p.bn) tc::tmem_ld_32x32(at + 32 * c, v[c]);
+      tc::tmem_ld_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(acc_empty0);
+      const int row = r0 + 128 * int(rank) + lane_base + lane;
+      if (row < p.R) {
+        const int live = min(p.bn, p.M - n0) - c0;
+        T* y = static_cast<T*>(p.Y) + int64_t(n0 + c0) * p.ldy + row;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (32 * c + i < live) *y = from_f32<T>(__uint_as_float(v[c][i]));
+            y += p.ldy;
+          }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();          // both CTAs out of their loops: the abort flags are final
+  if (*abort_flag) {
+    // A wait gave up in one of the CTAs, which raised both flags.  (1) rank 0's MMAs land;
+    // (2) the producers exchange their fill counts and the one behind fills the phases the
+    // other filled (boxes at the origin), so every phase of rank 0's full barriers that either
+    // CTA loaded into completes; (3) rank 0 waits for them, i.e. for both CTAs' copies;
+    // (4) neither CTA exits before that.
+    if (warp == 1 && rank == 0) {    // by the lane that issued the MMAs
+      if (tc::elect_one()) {
+        tc::mma_commit_pair(drain, 0x1);
+        tc::mbar_drain(drain, 0);
+      }
+      __syncwarp();
+    }
+    if (warp == 0 && lane == 0)
+      tc::st_cluster_u32(tc::cluster_addr(issued_slot, rank ^ 1u), uint32_t(issued));
+    tc::fence_before_sync();
+    tc::cluster_sync();
+    if (warp == 0 && lane == 0) {
+      const int64_t other = int64_t(*issued_slot);
+      for (int64_t f = issued; f < other; ++f) load(int(f % STAGES), 0, 0, 0);
+      if (rank == 0) tc::drain_tma_ring(full, STAGES, other > issued ? other : issued);
+    }
+    tc::fence_before_sync();
+    tc::cluster_sync();
+    if (threadIdx.x == 0 && rank == 0) raise_status(status, GPTQ_ERR_TIMEOUT);
+  }
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+}  // namespace pair
+
+// ------------------------------------------------------------------ host
+// rows of `row_bytes` bytes of codes, boxes of 128 bytes x box_rows
 bool encode_codes(CUtensorMap* m, const uint32_t* codes, uint64_t row_bytes, uint64_t rows,
                   uint32_t box_rows) {
   EncodeTiledFn enc = encode_tiled_fn();
@@ -192,31 +488,85 @@ bool encode_codes(CUtensorMap* m, const uint32_t* codes, uint64_t row_bytes, uin
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// scale tiles as rows (128 matrix rows) of ct * 512 bytes, boxes of two tiles x box_rows;
+// tiles past the ends read as zeros
+bool encode_scales(CUtensorMap* m, const uint8_t* scales, uint64_t ct, uint64_t tile_rows,
+                   uint32_t box_rows) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {ct * 128, tile_rows};
+  const cuuint64_t strides[1] = {ct * 512};
+  const cuuint32_t box[2] = {256, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<uint8_t*>(scales), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN, typename T>
-gptq_status launch(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, uint64_t row_bytes,
-                   const Prob& p, int32_t* status) {
-  using C = Cfg<BN>;
+gptq_status launch_few(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, uint64_t row_bytes,
+                       const Prob& p, int sms, int32_t* status) {
+  using C = Few<BN>;
   CUtensorMap wmap, xmap;
-  if (!encode_codes(&wmap, wc, row_bytes, uint64_t(p.R), TM) ||
+  if (!encode_codes(&wmap, wc, row_bytes, uint64_t(p.R), 128) ||
       !encode_codes(&xmap, xc, row_bytes, uint64_t(p.M), BN))
     return GPTQ_ERR_UNSUPPORTED;
-  // idesc: 4-bit codes on both sides, K-major, byte scales 2^(e-127), N = BN, M = 128
-  const uint32_t idesc = (1u << 7) | (1u << 10) | (uint32_t(BN >> 3) << 17) | (1u << 23) |
-                         (uint32_t(TM >> 4) << 24);
-  GPTQ_CUDA(allow_smem(k_mx_matmul<BN, T>, C::SMEM));
-  const dim3 grid((p.R + TM - 1) / TM, (p.M + BN - 1) / BN);
-  GPTQ_LAUNCH((k_mx_matmul<BN, T>), grid, THREADS, C::SMEM, st, wmap, xmap, p, idesc, status);
+  const int rows = (p.R + 127) / 128, cols = (p.M + BN - 1) / BN;
+  int splits = 1;
+  while (splits < 8 && int64_t(rows) * cols * splits * 2 <= sms && p.boxes >= 2 * C::SUB * splits)
+    splits *= 2;
+  GPTQ_CUDA(allow_smem(k_mx_few<BN, T>, C::SMEM));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(rows * splits), unsigned(cols));
+  cfg.blockDim = dim3(FEW_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(splits);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  GPTQ_CUDA(cudaLaunchKernelEx(&cfg, k_mx_few<BN, T>, wmap, xmap, p, status));
+  note_launch();
+  return GPTQ_OK;
+}
+
+template <typename T>
+gptq_status launch_pair(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, uint64_t row_bytes,
+                        Prob p, int sms, int32_t* status) {
+  CUtensorMap wmap, xmap, wsmap, xsmap;
+  if (!encode_codes(&wmap, wc, row_bytes, uint64_t(p.R), 128) ||
+      !encode_codes(&xmap, xc, row_bytes, uint64_t(p.M), uint32_t(p.bn / 2)) ||
+      !encode_scales(&wsmap, p.ws, uint64_t(p.ct), uint64_t((p.R + 127) / 128), 1) ||
+      !encode_scales(&xsmap, p.xs, uint64_t(p.ct), uint64_t((p.M + 127) / 128), uint32_t(p.nb)))
+    return GPTQ_ERR_UNSUPPORTED;
+  GPTQ_CUDA(allow_smem(pair::k_mx_pair<T>, pair::SMEM));
+  const int pairs = int(std::min<int64_t>(sms / 2, int64_t(p.ntr) * p.ntt));
+  GPTQ_LAUNCH(pair::k_mx_pair<T>, 2 * pairs, pair::THREADS, pair::SMEM, st, wmap, xmap, wsmap, xsmap,
+              p, idesc_of(256, p.bn), status);
   return GPTQ_OK;
 }
 
 template <typename T>
 gptq_status by_tokens(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, uint64_t row_bytes,
-                      const Prob& p, int32_t* status) {
-  if (p.M <= 16) return launch<16, T>(st, xc, wc, row_bytes, p, status);
-  if (p.M <= 32) return launch<32, T>(st, xc, wc, row_bytes, p, status);
-  if (p.M <= 64) return launch<64, T>(st, xc, wc, row_bytes, p, status);
-  if (p.M <= 128) return launch<128, T>(st, xc, wc, row_bytes, p, status);
-  return launch<256, T>(st, xc, wc, row_bytes, p, status);
+                      Prob p, int sms, int32_t* status) {
+  if (p.M <= 16) return launch_few<16, T>(st, xc, wc, row_bytes, p, sms, status);
+  if (p.M <= 32) return launch_few<32, T>(st, xc, wc, row_bytes, p, sms, status);
+  if (p.M <= 64) return launch_few<64, T>(st, xc, wc, row_bytes, p, sms, status);
+  if (p.M <= 128) return launch_few<128, T>(st, xc, wc, row_bytes, p, sms, status);
+  // the widest token tile by the time of the pairs' waves: a tile's step takes about
+  // 64 + bn/4 cycles (shared memory moves 4 KB of W and bn/64 KB of X in and out)
+  int64_t best = 0;
+  p.ntr = (p.R + 255) / 256;
+  for (int bn = 256; bn >= 64; bn -= 32) {
+    const int64_t tiles = int64_t(p.ntr) * ((p.M + bn - 1) / bn), pairs = sms / 2;
+    const int64_t time = (tiles + pairs - 1) / pairs * (64 + bn / 4);
+    if (best == 0 || time < best) { best = time; p.bn = bn; }
+  }
+  p.nb = p.bn % 128 == 0 ? p.bn / 128 : (p.bn + 96 + 127) / 128;
+  p.ntt = (p.M + p.bn - 1) / p.bn;
+  return launch_pair<T>(st, xc, wc, row_bytes, p, sms, status);
 }
 
 }  // namespace
@@ -224,8 +574,10 @@ gptq_status by_tokens(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, u
 gptq_status mx_matmul_run(cudaStream_t st, const uint32_t* xc, const uint8_t* xs, int M,
                           const uint32_t* wc, const uint8_t* ws, int R, int C, void* Y, int dt,
                           int64_t ldy, int32_t* status) {
+  const int sms = sm_count();
+  if (sms <= 0) return GPTQ_ERR_CUDA;
   const int nb = (C + 31) / 32;
-  Prob p;
+  Prob p = {};
   p.xs = xs;
   p.ws = ws;
   p.Y = Y;
@@ -234,12 +586,13 @@ gptq_status mx_matmul_run(cudaStream_t st, const uint32_t* xc, const uint8_t* xs
   p.R = R;
   p.steps = (nb + 1) / 2;
   p.ct = (nb + 3) / 4;
+  p.boxes = (nb + 7) / 8;
   p.wait_limit = pipeline_wait_limit();
   const uint64_t row_bytes = uint64_t(nb) * 16;
   switch (dt) {
-    case GPTQ_F32: return by_tokens<float>(st, xc, wc, row_bytes, p, status);
-    case GPTQ_F16: return by_tokens<__half>(st, xc, wc, row_bytes, p, status);
-    default: return by_tokens<__nv_bfloat16>(st, xc, wc, row_bytes, p, status);
+    case GPTQ_F32: return by_tokens<float>(st, xc, wc, row_bytes, p, sms, status);
+    case GPTQ_F16: return by_tokens<__half>(st, xc, wc, row_bytes, p, sms, status);
+    default: return by_tokens<__nv_bfloat16>(st, xc, wc, row_bytes, p, sms, status);
   }
 }
 
