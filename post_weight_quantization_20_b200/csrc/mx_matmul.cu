@@ -208,15 +208,28 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
   if (splits > 1) {
     // every CTA of the cluster sums its share of the tokens, the splits in order
     tc::cluster_sync();
-    if (warp >= 2) {
-      const int i = (warp & 3) * 32 + lane, row = r0 + i;
-      const int live = min(BN, p.M - n0);
-      for (int t = split; t < live; t += splits) {
-        float v = 0.f;
-        for (int q = 0; q < splits; ++q)
-          v += tc::ld_cluster_f32(tc::cluster_addr(smem + (t * 128 + i) * 4, uint32_t(q)));
-        if (row < p.R) static_cast<T*>(p.Y)[int64_t(n0 + t) * p.ldy + row] = from_f32<T>(v);
-      }
+    // (a warp a token, a lane four layer rows, all loads before the first sum)
+    const int live = min(BN, p.M - n0), row = r0 + 4 * lane;
+    for (int t = split + splits * warp; t < live; t += splits * (FEW_THREADS / 32)) {
+      const uint32_t at = tc::smem_u32(smem + (t * 128 + 4 * lane) * 4);
+      float4 part[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (q < splits) part[q] = tc::ld_cluster_f32x4(tc::map_cluster(at, uint32_t(q)));
+      float4 v = part[0];
+#pragma unroll
+      for (int q = 1; q < 8; ++q)
+        if (q < splits) {
+          v.x += part[q].x;
+          v.y += part[q].y;
+          v.z += part[q].z;
+          v.w += part[q].w;
+        }
+      T* y = static_cast<T*>(p.Y) + int64_t(n0 + t) * p.ldy + row;
+      const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row + i < p.R) y[i] = from_f32<T>(o[i]);
     }
     __syncwarp();
     tc::cluster_sync();                // no CTA leaves while its partial sums are read

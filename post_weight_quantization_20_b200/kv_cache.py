@@ -20,7 +20,7 @@ from dataclasses import dataclass
 import torch
 
 from . import gptq as G
-from .mx import _on_device, _p, _stream, mx_words
+from .mx import _WORDS, _call, _expect, _need_one_device, _status_ptr, mx_words
 
 GPTQ_CACHE_GRID, GPTQ_CACHE_MX = 0, 1
 
@@ -96,17 +96,17 @@ def _words(cfg, dim):
     return mx_words(dim) if cfg.kind == GPTQ_CACHE_MX else G.packed_words(dim, cfg.bits)
 
 
-def _expect_rows_of(t, name, like=None):
+def _expect_rows_of(t, name):
     if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
         raise ValueError(f"{name} must be 3-D (rows, heads, dim) with unit stride along dim")
     if t.dtype not in G._DT:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{name} must have the shape and dtype of K")
 
 
 def _no_overlap(t, name):
     """Written tensors: no two (row, head) pairs may share memory."""
+    if t.is_contiguous():
+        return
     n, h, d = t.shape
     (a, sa), (b, sb) = sorted(((n, t.stride(0)), (h, t.stride(1))), key=lambda x: x[1])
     if (a > 1 and sa < d) or (b > 1 and sb < (sa * (a - 1) + d if a > 1 else d)):
@@ -115,60 +115,59 @@ def _no_overlap(t, name):
 
 def _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, status,
              written=False):
+    """Check a call's tensors; the arguments of the C call that both directions share."""
     _expect_rows_of(K, "K")
-    _expect_rows_of(V, "V", K)
+    _expect_rows_of(V, "V")
+    if V.shape != K.shape or V.dtype != K.dtype:
+        raise ValueError("V must have the shape and dtype of K")
     if written:
         _no_overlap(K, "K")
         _no_overlap(V, "V")
     T, H, D = K.shape
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be 4-D (pages, page_size, heads, words)")
-    pages, page_size = k_codes.shape[:2]
-    words = (torch.int32, torch.uint32)
-    G._expect(k_codes, "k_codes", (pages, page_size, H, _words(cfg, D)), words)
-    G._expect(v_codes, "v_codes", (pages, page_size, H, _words(cfg, D)), words)
+    pages, page_size, _, _ = k_codes.shape
+    shape = (pages, page_size, H, _words(cfg, D))
+    _expect(k_codes, "k_codes", shape, _WORDS)
+    _expect(v_codes, "v_codes", shape, _WORDS)
     shape, dtype = _grid_shape(cfg, pages, page_size, H, D)
-    G._expect(k_grids, "k_grids", shape, (dtype,))
-    G._expect(v_grids, "v_grids", shape, (dtype,))
+    _expect(k_grids, "k_grids", shape, (dtype,))
+    _expect(v_grids, "v_grids", shape, (dtype,))
     if table.dim() != 2 or table.dtype != torch.int32 or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("table must be an int32 (seqs, width) tensor with unit column stride")
     S, width = table.shape
-    if S > 1 and table.stride(0) < width:
+    ld = table.stride(0) if S > 1 else width
+    if ld < width:
         raise ValueError("the rows of table must not overlap")
-    G._expect(cu, "cu", (S + 1,), (torch.int32,))
-    G._expect(start, "start", (S,), (torch.int32,))
-    G._expect_status(status)
-    G._need_cuda(K, V, k_codes, k_grids, v_codes, v_grids, table, cu, start, status)
+    _expect(cu, "cu", (S + 1,), (torch.int32,))
+    _expect(start, "start", (S,), (torch.int32,))
+    st = _status_ptr(status)
+    _need_one_device(K, V, k_codes, k_grids, v_codes, v_grids, table, cu, start, status)
     cache = gptq_cache(k_codes.data_ptr(), k_grids.data_ptr(), v_codes.data_ptr(),
                        v_grids.data_ptr(), pages, page_size, H, D)
-    rows = gptq_cache_rows(table.data_ptr(), table.stride(0) if S > 1 else width, width,
-                           cu.data_ptr(), start.data_ptr(), S)
-    strides = (K.stride(0), K.stride(1), V.stride(0), V.stride(1))
-    return cache, rows, T, strides
+    rows = gptq_cache_rows(table.data_ptr(), ld, width, cu.data_ptr(), start.data_ptr(), S)
+    where = (ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rows))
+    (kt, kh, _), (vt, vh, _) = K.stride(), V.stride()
+    data = (K.data_ptr(), V.data_ptr(), G._DT[K.dtype], T, kt, kh, vt, vh)
+    return where, data, st
 
 
 def gptq_cache_write(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, status=None,
                      stream=None) -> None:
     """Quantise the rows of K and V (rows, heads, dim) into their slots of the cache."""
-    cache, rows, T, strides = _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu,
-                                       start, status)
-    with _on_device(K):
-        G._check(load_library().gptq_cache_write(
-            K.data_ptr(), V.data_ptr(), G._DT[K.dtype], T, *strides, ctypes.byref(cfg),
-            ctypes.byref(cache), ctypes.byref(rows), _p(status), _stream(stream, K)),
-            "gptq_cache_write")
+    where, data, st = _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start,
+                               status)
+    load_library()
+    _call("gptq_cache_write", K, stream, *data, *where, st)
 
 
 def gptq_cache_read(cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, K, V, status=None,
                     stream=None) -> None:
     """The rows' values out of their slots of the cache into K and V (rows, heads, dim)."""
-    cache, rows, T, strides = _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu,
-                                       start, status, written=True)
-    with _on_device(K):
-        G._check(load_library().gptq_cache_read(
-            ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rows), K.data_ptr(),
-            V.data_ptr(), G._DT[K.dtype], T, *strides, _p(status), _stream(stream, K)),
-            "gptq_cache_read")
+    where, data, st = _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start,
+                               status, written=True)
+    load_library()
+    _call("gptq_cache_read", K, stream, *where, *data, st)
 
 
 # --------------------------------------------------------------------------- one cache

@@ -12,7 +12,6 @@ stream of the tensors' device) and nothing is synchronised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -57,80 +56,103 @@ def gptq_mx_scale_bytes(rows: int, cols: int) -> int:
     return int(load_library().gptq_mx_scale_bytes(rows, cols))
 
 
-def _on_device(t: torch.Tensor):
-    """Make t's device the current one: a launch and its stream belong to it."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+_WORDS = (torch.int32, torch.uint32)
 
 
-def _stream(stream, t: torch.Tensor):
-    s = torch.cuda.current_stream(t.device) if stream is None else stream
-    return s.cuda_stream
+def _call(name, where, stream, *args):
+    """Call the library on `stream` of the device of the tensor `where`, which is made the
+    current one (a launch and its stream belong to it)."""
+    dev = where.get_device()
+    f = getattr(load_library(), name)
+    if dev == torch._C._cuda_getDevice():
+        code = f(*args, _raw_stream(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, _raw_stream(stream, dev))
+    if code:
+        G._check(code, name)
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _need_one_device(first, *others):
+    """Device tensors, all on one device (None is left out)."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            break
+    else:
+        if dev >= 0:
+            return
+    G._need_cuda(first, *others)
+
+
+def _expect(t, name, shape, dtypes):
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
+        G._expect(t, name, shape, dtypes)
 
 
 def _expect_matrix(t, name):
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    """Rows and columns of a matrix, its type and the distance of its rows."""
+    if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with unit column stride")
-    if t.dtype not in G._DT:
+    (R, C), (ld, one) = t.shape, t.stride()
+    if one != 1 and C > 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    dt = G._DT.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if R <= 1:
+        ld = C
+    elif ld < C:
         raise ValueError(f"the rows of {name} must not overlap")
+    return R, C, dt, ld
 
 
 def _expect_stored(codes, scales, rows, cols, name=""):
-    G._expect(codes, name + "codes", (rows, mx_words(cols)), (torch.int32, torch.uint32))
-    G._expect(scales, name + "scales", mx_scale_shape(rows, cols), (torch.uint8,))
+    _expect(codes, name + "codes", (rows, mx_words(cols)), _WORDS)
+    _expect(scales, name + "scales", mx_scale_shape(rows, cols), (torch.uint8,))
 
 
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
+def _status_ptr(status):
+    if status is None:
+        return None
+    G._expect_status(status)
+    return status.data_ptr()
 
 
 def gptq_mx_quantize(X, codes, scales, status=None, stream=None) -> None:
     """The stored form of X (rows x cols, unit column stride) into codes and scales."""
-    _expect_matrix(X, "X")
-    R, C = X.shape
+    R, C, dt, ld = _expect_matrix(X, "X")
     _expect_stored(codes, scales, R, C)
-    G._expect_status(status)
-    G._need_cuda(X, codes, scales, status)
-    with _on_device(X):
-        G._check(load_library().gptq_mx_quantize(X.data_ptr(), G._DT[X.dtype], R, C, _ld(X),
-                                                 codes.data_ptr(), scales.data_ptr(), _p(status),
-                                                 _stream(stream, X)), "gptq_mx_quantize")
+    st = _status_ptr(status)
+    _need_one_device(X, codes, scales, status)
+    _call("gptq_mx_quantize", X, stream, X.data_ptr(), dt, R, C, ld, codes.data_ptr(),
+          scales.data_ptr(), st)
 
 
 def gptq_mx_dequantize(codes, scales, Y, stream=None) -> None:
     """Y (rows x cols) = the values the stored form stands for."""
-    _expect_matrix(Y, "Y")
-    R, C = Y.shape
+    R, C, dt, ld = _expect_matrix(Y, "Y")
     _expect_stored(codes, scales, R, C)
-    G._need_cuda(codes, scales, Y)
-    with _on_device(Y):
-        G._check(load_library().gptq_mx_dequantize(codes.data_ptr(), scales.data_ptr(), R, C,
-                                                   Y.data_ptr(), G._DT[Y.dtype], _ld(Y),
-                                                   _stream(stream, Y)), "gptq_mx_dequantize")
+    _need_one_device(Y, codes, scales)
+    _call("gptq_mx_dequantize", Y, stream, codes.data_ptr(), scales.data_ptr(), R, C,
+          Y.data_ptr(), dt, ld)
 
 
 def gptq_mx_matmul(x_codes, x_scales, w_codes, w_scales, cols, Y, status=None,
                    stream=None) -> None:
     """Y (tokens x rows) = X W^T of two stored forms with `cols` columns each."""
-    _expect_matrix(Y, "Y")
-    M, R = Y.shape
+    M, R, dt, ld = _expect_matrix(Y, "Y")
     cols = int(cols)
     _expect_stored(x_codes, x_scales, M, cols, "x_")
     _expect_stored(w_codes, w_scales, R, cols, "w_")
-    G._expect_status(status)
-    G._need_cuda(x_codes, x_scales, w_codes, w_scales, Y, status)
-    with _on_device(Y):
-        G._check(load_library().gptq_mx_matmul(
-            x_codes.data_ptr(), x_scales.data_ptr(), M, w_codes.data_ptr(), w_scales.data_ptr(),
-            R, cols, Y.data_ptr(), G._DT[Y.dtype], _ld(Y), _p(status), _stream(stream, Y)),
-            "gptq_mx_matmul")
+    st = _status_ptr(status)
+    _need_one_device(Y, x_codes, x_scales, w_codes, w_scales, status)
+    _call("gptq_mx_matmul", Y, stream, x_codes.data_ptr(), x_scales.data_ptr(), M,
+          w_codes.data_ptr(), w_scales.data_ptr(), R, cols, Y.data_ptr(), dt, ld, st)
 
 
 # --------------------------------------------------------------------------- whole matrices
