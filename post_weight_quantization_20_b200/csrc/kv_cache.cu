@@ -19,7 +19,8 @@ namespace gptq {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int STEPS = 4;          // rows of a thread whose loads are issued together
+constexpr int STEPS = 4;          // rows of a thread whose loads are issued together in a read
+constexpr int AHEAD = 2;          // rows that a write loads ahead
 
 struct Args {
   const void* in[2];     // write: K and V
@@ -65,32 +66,53 @@ __device__ __forceinline__ int64_t find_slot(const Args& a, int64_t t, int32_t* 
 
 enum { GRID4 = 0, GRID8 = 1, MX4 = 2 };
 
-// Codes of N values on a grid: clamp(rint(x / s) + z, 0, maxq) with the quotient rounded to
-// fp32.  x * (1/s) is within 2^-15 of that quotient for |x / s| <= 256 (half an ulp of the
-// quotient, and a relative 2^-24 for the reciprocal), so the two can round apart only that
-// near a half-integer; then, and for an s whose reciprocal leaves fp32's range, all of the
-// lane's values are divided.  Adding 1.5 * 2^23 rounds to a whole number, which is read off
-// the sum's low bits.
-template <int N>
-__device__ __forceinline__ void grid_codes(const float (&x)[N], float s, float z, int maxq,
-                                           int (&c)[N]) {
-  constexpr float magic = 12582912.f;
-  const float inv = __frcp_rn(s);
-  const int zi = int(z);
-  float near = 0.f;
+// x / s rounded to fp32 where nothing under- or overflows, without a division: with inv = 1 / s
+// rounded, x * inv is within 1.5 ulp of the quotient, a residual correction brings it within
+// one, and from there a second one gives the correctly rounded quotient (Markstein, IBM J. Res.
+// Dev. 34(1), 1990).  The codes need that rounding: 16-bit values hit exact ties of their grid
+// all the time (15 x / (hi - lo) is a fraction of small whole numbers).  The division itself
+// per value took twice as long (470 us against 240 for 131072 tokens of 8 x 128 bf16 K and V).
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, s, x), inv, q);
+  return fmaf(fmaf(-q, s, x), inv, q);
+}
+
+// The grid of [lo, hi] and the codes clamp(rint(x / s) + z, 0, maxq) of N values on it, as
+// grid_params defines it; false if the range is not finite.
+template <int N, int maxq>
+__device__ __forceinline__ bool grid_codes(const float (&x)[N], float lo, float hi, int sym, float& s,
+                                           float& z, int (&c)[N]) {
+  const float m = fmaxf(-lo, hi);
+  const float width = sym ? m + m : hi - lo;
+  // no under- or overflow below (not taken by NaN either)
+  if (width > 0x1p-90f && width < 0x1p90f) {
+    s = quotient(width, float(maxq), 1.f / float(maxq));
+    const float inv = __frcp_rn(s);
+    // adding 1.5 * 2^23 rounds to a whole number, which is the sum's low bits
+    constexpr float magic = 12582912.f;
+    constexpr int magic_bits = 0x4B400000;
+    const int zi = sym ? (maxq + 1) / 2
+                       : __float_as_int(quotient(-lo, s, inv) + magic) - magic_bits;
+    z = sym ? float(zi) : copysignf(float(zi), -lo);      // a zero with the sign that rint(-lo / s) has
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float t = fmaf(x[i], inv, magic);
-    near = fmaxf(near, fabsf(fmaf(x[i], inv, magic - t)));
-    c[i] = __vimin_s32_relu(__float_as_int(t) - 0x4B400000 + zi, maxq);
+    for (int i = 0; i < N; ++i)
+      c[i] = __vimin_s32_relu(__float_as_int(quotient(x[i], s, inv) + magic) + (zi - magic_bits), maxq);
+    return true;
   }
-  if (near > 0.49995f || s < 0x1p-100f || s > 0x1p100f) {
+  grid_params(lo, hi, float(maxq), sym, s, z);
+  if (s == 0.f) grid_params(-1.f, 1.f, float(maxq), sym, s, z);     // an underflowed range
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float r = rintf(__fdiv_rn(x[i], s));
-      c[i] = int(fminf(fmaxf(r + z, 0.f), float(maxq)));
-    }
+  for (int i = 0; i < N; ++i) c[i] = 0;
+  if (lo != lo || !(s <= 3.402823466e38f)) {
+    s = __uint_as_float(0x7FC00000u);
+    z = 0.f;
+    return false;
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    c[i] = int(fminf(fmaxf(rintf(__fdiv_rn(x[i], s)) + z, 0.f), float(maxq)));
+  return true;
 }
 
 template <typename T, int KIND>
@@ -107,27 +129,31 @@ k_cache_write(const Args a, int32_t* status) {
   const T* in = static_cast<const T*>(a.in[pl.kv]) + t0 * a.ldt[pl.kv] + pl.head * a.ldh[pl.kv] + first;
   const int64_t ldt = a.ldt[pl.kv];
   bool bad = false;
-  for (int r0 = 0; r0 < rows; r0 += STEPS * a.side) {
-    U unit[STEPS];
+  // the next AHEAD rows are loading while a row is quantised (one copy of that code: unrolled
+  // over the rows it no longer fits the instruction cache)
+  U unit[AHEAD];
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int r = r0 + s * a.side + pl.row;
-      unit[s].load(in + r * ldt, r < rows ? n : 0, a.vec != 0);
-    }
-    if (r0 == 0) {
-      if (int(threadIdx.x) < rows) slots[threadIdx.x] = find_slot(a, t0 + threadIdx.x, status);
-      __syncthreads();
-    }
+  for (int s = 0; s < AHEAD; ++s) {
+    const int r = s * a.side + pl.row;
+    unit[s].load(in + r * ldt, r < rows ? n : 0, a.vec != 0);
+  }
+  if (int(threadIdx.x) < rows) slots[threadIdx.x] = find_slot(a, t0 + threadIdx.x, status);
+  __syncthreads();
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += a.side) {
+    const U now = unit[0];
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int r = r0 + s * a.side + pl.row;
+    for (int s = 0; s + 1 < AHEAD; ++s) unit[s] = unit[s + 1];
+    const int r = r0 + pl.row, rn = r + AHEAD * a.side;
+    unit[AHEAD - 1].load(in + rn * ldt, rn < rows ? n : 0, a.vec != 0);
+    {
       const int64_t slot = r < rows && pl.live ? slots[r] : -1;
       const int64_t head = slot * a.heads + pl.head;
       uint32_t* codes = a.codes[pl.kv] + head * a.words + first / (KIND == GRID8 ? 4 : 8);
       float v[U::N];
-      unit[s].widen(v);
+      now.widen(v);
       if constexpr (KIND == MX4) {
-        uint32_t m = unit[s].amax_bits();
+        uint32_t m = now.amax_bits();
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         if (U::N == 8) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const int e = mx::scale_byte(m);
@@ -147,7 +173,7 @@ k_cache_write(const Args a, int32_t* status) {
       } else {
         constexpr int maxq = KIND == GRID4 ? 15 : 255;
         float lo, hi;
-        unit[s].range(lo, hi);
+        now.range(lo, hi);
         for (int o = 1; o < (1 << a.lane_bits); o <<= 1) {
           lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
           hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
@@ -155,18 +181,8 @@ k_cache_write(const Args a, int32_t* status) {
         lo = min_nan(lo, 0.f);
         hi = max_nan(hi, 0.f);
         float sc, z;
-        grid_params(lo, hi, float(maxq), a.sym, sc, z);
-        if (sc == 0.f) grid_params(-1.f, 1.f, float(maxq), a.sym, sc, z);   // an underflowed range
-        const bool nan = lo != lo || !(sc <= 3.402823466e38f);
         int c[U::N];
-        if (nan) {
-          sc = __uint_as_float(0x7FC00000u);
-          z = 0.f;
-#pragma unroll
-          for (int j = 0; j < U::N; ++j) c[j] = 0;
-        } else {
-          grid_codes<U::N>(v, sc, z, maxq, c);
-        }
+        const bool nan = !grid_codes<U::N, maxq>(v, lo, hi, a.sym, sc, z, c);
         if (slot >= 0 && n > 0) {
           bad |= nan;
           // 8 codes at a time: all of dim, which is a multiple of 8, and no more
@@ -175,7 +191,7 @@ k_cache_write(const Args a, int32_t* status) {
             for (int j = 0; j < U::WORDS; ++j) {
               uint32_t w = 0;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w |= uint32_t(c[8 * j + i]) << (4 * i);
+              for (int i = 0; i < 8; ++i) w += uint32_t(c[8 * j + i]) << (4 * i);
               if (8 * j < n) codes[j] = w;
             }
           } else {
@@ -183,7 +199,7 @@ k_cache_write(const Args a, int32_t* status) {
             for (int j = 0; j < U::WORDS; ++j) {
               uint32_t w[2] = {0u, 0u};
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w[i >> 2] |= uint32_t(c[8 * j + i]) << (8 * (i & 3));
+              for (int i = 0; i < 8; ++i) w[i >> 2] += uint32_t(c[8 * j + i]) << (8 * (i & 3));
               if (8 * j < n) *reinterpret_cast<uint2*>(codes + 2 * j) = make_uint2(w[0], w[1]);
             }
           }
@@ -248,11 +264,13 @@ k_cache_read(const Args a, int32_t* status) {
 #pragma unroll
         for (int j = 0; j < O::N; ++j) v[j] *= g[s].x;
       } else {
-        // the code as a float without a conversion: 2^23 + c, less 2^23 (exact)
+        // the code as a float without a conversion: 2^23 + c, less 2^23 + z; both are whole
+        // numbers below 2^24 (z < 2^10 on any grid that a write stores), the difference exact
+        const float zz = 8388608.f + g[s].y;
 #pragma unroll
         for (int j = 0; j < O::N; ++j) {
           const uint32_t c = KIND == GRID4 ? (w[s][0] >> (4 * j)) & 15u : (w[s][j >> 2] >> (8 * (j & 3))) & 255u;
-          v[j] = g[s].x * ((__uint_as_float(0x4B000000u | c) - 8388608.f) - g[s].y);
+          v[j] = g[s].x * (__uint_as_float(0x4B000000u | c) - zz);
         }
       }
       O::store(out + (r0 + s * a.side) * ldt, O::N, a.vec != 0, v);
@@ -274,10 +292,10 @@ gptq_status launch(cudaStream_t st, bool write, Args& a, int32_t* status) {
   if (parts > 65535) return GPTQ_ERR_UNSUPPORTED;
   a.per_row = int(per_row);
   a.side = std::max(1, THREADS / a.per_row);
-  // rows of a CTA: two rounds of loads per thread where that leaves four CTAs per SM, and
-  // one row per thread at least
-  const int64_t want = a.tokens * parts / (4 * 148);
-  a.rows = int(std::min<int64_t>(THREADS, a.side * std::max<int64_t>(1, std::min<int64_t>(2 * STEPS, want / a.side))));
+  // rows of a CTA: enough to pay for finding their slots where that leaves eight CTAs per SM,
+  // and one row per thread at least
+  const int64_t want = a.tokens * parts / (8 * 148);
+  a.rows = int(std::min<int64_t>(THREADS, a.side * std::max<int64_t>(1, std::min<int64_t>(32, want / a.side))));
   const int64_t blocks = (a.tokens + a.rows - 1) / a.rows;
   const dim3 grid{unsigned(blocks), unsigned(parts)};
   if (write) GPTQ_LAUNCH((k_cache_write<T, KIND>), grid, THREADS, 0, st, a, status);
