@@ -57,11 +57,15 @@ struct Place {
   }
 };
 
-// The slot of row t, negative if it has none.  Reported by the first part of a row only.
-__device__ __forceinline__ int64_t find_slot(const Args& a, int64_t t, int32_t* status) {
+// Where row t is stored: its first word of codes and its first group, or negative if nowhere
+// (reported by the first part of a row only).
+struct Where {
+  int64_t word, group;
+};
+__device__ __forceinline__ Where find_row(const Args& a, int64_t t, int32_t* status) {
   const int64_t slot = slot_of(a.map, t);
   if (slot == SLOT_BAD && blockIdx.y == 0) raise_status(status, GPTQ_ERR_INVALID_ARG);
-  return slot;
+  return {slot < 0 ? -1 : slot * (int64_t(a.heads) * a.words), slot * (int64_t(a.heads) * a.groups)};
 }
 
 enum { GRID4 = 0, GRID8 = 1, MX4 = 2 };
@@ -119,7 +123,7 @@ template <typename T, int KIND>
 __global__ void __launch_bounds__(THREADS)
 k_cache_write(const Args a, int32_t* status) {
   using U = Unit<T>;
-  __shared__ int64_t slots[THREADS];
+  __shared__ Where stored[THREADS];
   const Place pl(a);
   const int64_t t0 = int64_t(blockIdx.x) * a.rows;
   const int rows = int(min(int64_t(a.rows), a.tokens - t0));
@@ -128,6 +132,8 @@ k_cache_write(const Args a, int32_t* status) {
   const int n = pl.live ? a.dim - first : 0;
   const T* in = static_cast<const T*>(a.in[pl.kv]) + t0 * a.ldt[pl.kv] + pl.head * a.ldh[pl.kv] + first;
   const int64_t ldt = a.ldt[pl.kv];
+  uint32_t* codes0 = a.codes[pl.kv] + int64_t(pl.head) * a.words + first / (KIND == GRID8 ? 4 : 8);
+  const int64_t group0 = int64_t(pl.head) * a.groups + group;
   bool bad = false;
   // the next AHEAD rows are loading while a row is quantised (one copy of that code: unrolled
   // over the rows it no longer fits the instruction cache)
@@ -137,7 +143,7 @@ k_cache_write(const Args a, int32_t* status) {
     const int r = s * a.side + pl.row;
     unit[s].load(in + r * ldt, r < rows ? n : 0, a.vec != 0);
   }
-  if (int(threadIdx.x) < rows) slots[threadIdx.x] = find_slot(a, t0 + threadIdx.x, status);
+  if (int(threadIdx.x) < rows) stored[threadIdx.x] = find_row(a, t0 + threadIdx.x, status);
   __syncthreads();
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += a.side) {
@@ -147,9 +153,9 @@ k_cache_write(const Args a, int32_t* status) {
     const int r = r0 + pl.row, rn = r + AHEAD * a.side;
     unit[AHEAD - 1].load(in + rn * ldt, rn < rows ? n : 0, a.vec != 0);
     {
-      const int64_t slot = r < rows && pl.live ? slots[r] : -1;
-      const int64_t head = slot * a.heads + pl.head;
-      uint32_t* codes = a.codes[pl.kv] + head * a.words + first / (KIND == GRID8 ? 4 : 8);
+      Where at = {-1, 0};
+      if (r < rows && pl.live) at = stored[r];
+      uint32_t* codes = codes0 + at.word;
       float v[U::N];
       now.widen(v);
       if constexpr (KIND == MX4) {
@@ -163,12 +169,12 @@ k_cache_write(const Args a, int32_t* status) {
         for (int j = 0; j < U::N; ++j) v[j] *= f;
 #pragma unroll
         for (int j = 0; j < U::WORDS; ++j) w[j] = e == 255 ? 0u : mx::encode8(v + 8 * j);
-        if (slot >= 0) {
+        if (at.word >= 0) {
           bad |= e == 255;
           if constexpr (U::WORDS == 2) *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
           else *codes = w[0];
           if ((first & 31) == 0)
-            static_cast<uint8_t*>(a.grids[pl.kv])[head * a.groups + group] = uint8_t(e);
+            static_cast<uint8_t*>(a.grids[pl.kv])[at.group + group0] = uint8_t(e);
         }
       } else {
         constexpr int maxq = KIND == GRID4 ? 15 : 255;
@@ -183,7 +189,7 @@ k_cache_write(const Args a, int32_t* status) {
         float sc, z;
         int c[U::N];
         const bool nan = !grid_codes<U::N, maxq>(v, lo, hi, a.sym, sc, z, c);
-        if (slot >= 0 && n > 0) {
+        if (at.word >= 0 && n > 0) {
           bad |= nan;
           // 8 codes at a time: all of dim, which is a multiple of 8, and no more
           if constexpr (KIND == GRID4) {
@@ -204,7 +210,7 @@ k_cache_write(const Args a, int32_t* status) {
             }
           }
           if (pl.lane == group << a.lane_bits)
-            static_cast<float2*>(a.grids[pl.kv])[head * a.groups + group] = make_float2(sc, z);
+            static_cast<float2*>(a.grids[pl.kv])[at.group + group0] = make_float2(sc, z);
         }
       }
     }
@@ -216,16 +222,15 @@ template <typename T, int KIND>
 __global__ void __launch_bounds__(THREADS)
 k_cache_read(const Args a, int32_t* status) {
   using O = Out<T>;
-  __shared__ int64_t slots[THREADS];
+  __shared__ Where stored[THREADS];
   const Place pl(a);
   const int64_t t0 = int64_t(blockIdx.x) * a.rows;
   const int rows = int(min(int64_t(a.rows), a.tokens - t0));
-  if (int(threadIdx.x) < rows) slots[threadIdx.x] = find_slot(a, t0 + threadIdx.x, status);
+  if (int(threadIdx.x) < rows) stored[threadIdx.x] = find_row(a, t0 + threadIdx.x, status);
   const int first = pl.lane * O::N;
   const int group = first / a.group;
   const uint32_t* codes = a.codes[pl.kv] + int64_t(pl.head) * a.words + first / (KIND == GRID8 ? 4 : 8);
-  const int64_t per_slot = int64_t(a.heads) * a.words, grids_per_slot = int64_t(a.heads) * a.groups;
-  const int64_t grid0 = int64_t(pl.head) * a.groups + group;
+  const int64_t group0 = int64_t(pl.head) * a.groups + group;
   T* out = static_cast<T*>(a.out[pl.kv]) + t0 * a.ldt[pl.kv] + pl.head * a.ldh[pl.kv] + first;
   const int64_t ldt = a.ldt[pl.kv];
   __syncthreads();
@@ -237,10 +242,11 @@ k_cache_read(const Args a, int32_t* status) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       const int r = r0 + s * a.side;
-      const int64_t slot = r < rows ? slots[r] : -1;
-      live[s] = slot >= 0;
+      Where at = {-1, 0};
+      if (r < rows) at = stored[r];
+      live[s] = at.word >= 0;
       if (!live[s]) continue;
-      const uint32_t* p = codes + slot * per_slot;
+      const uint32_t* p = codes + at.word;
       if constexpr (KIND == GRID8 && O::N == 8) {
         const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
         w[s][0] = q.x;
@@ -249,9 +255,9 @@ k_cache_read(const Args a, int32_t* status) {
         w[s][0] = __ldg(p);
       }
       if constexpr (KIND == MX4)
-        g[s].x = mx::scale_value(__ldg(static_cast<const uint8_t*>(a.grids[pl.kv]) + slot * grids_per_slot + grid0));
+        g[s].x = mx::scale_value(__ldg(static_cast<const uint8_t*>(a.grids[pl.kv]) + at.group + group0));
       else
-        g[s] = __ldg(static_cast<const float2*>(a.grids[pl.kv]) + slot * grids_per_slot + grid0);
+        g[s] = __ldg(static_cast<const float2*>(a.grids[pl.kv]) + at.group + group0);
     }
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -264,13 +270,19 @@ k_cache_read(const Args a, int32_t* status) {
 #pragma unroll
         for (int j = 0; j < O::N; ++j) v[j] *= g[s].x;
       } else {
-        // the code as a float without a conversion: 2^23 + c, less 2^23 + z; both are whole
-        // numbers below 2^24 (z < 2^10 on any grid that a write stores), the difference exact
+        // the code as a float without a conversion: 2^23 + c (the code as the lowest byte of
+        // that float), less 2^23 + z; both are whole numbers below 2^24 (z < 2^10 on any grid
+        // that a write stores), the difference exact
         const float zz = 8388608.f + g[s].y;
+        if constexpr (KIND == GRID4) {             // even codes to bytes, odd ones to bytes
+          w[s][1] = (w[s][0] >> 4) & 0x0F0F0F0Fu;
+          w[s][0] &= 0x0F0F0F0Fu;
+        }
 #pragma unroll
         for (int j = 0; j < O::N; ++j) {
-          const uint32_t c = KIND == GRID4 ? (w[s][0] >> (4 * j)) & 15u : (w[s][j >> 2] >> (8 * (j & 3))) & 255u;
-          v[j] = g[s].x * (__uint_as_float(0x4B000000u | c) - zz);
+          const uint32_t from = KIND == GRID4 ? w[s][j & 1] : w[s][j >> 2];
+          const uint32_t byte = KIND == GRID4 ? j >> 1 : j & 3;
+          v[j] = g[s].x * (__uint_as_float(__byte_perm(from, 0x4B000000u, 0x7540u + byte)) - zz);
         }
       }
       O::store(out + (r0 + s * a.side) * ldt, O::N, a.vec != 0, v);
