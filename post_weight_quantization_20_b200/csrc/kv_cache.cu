@@ -14,13 +14,13 @@
 #include "kernels.h"
 #include "kv_slots.h"
 #include "mx.cuh"
+#include "tc_common.cuh"
 
 namespace gptq {
 namespace {
 
 constexpr int THREADS = 256;
 constexpr int STEPS = 4;          // rows of a thread whose loads are issued together in a read
-constexpr int AHEAD = 2;          // rows that a write loads ahead
 
 struct Args {
   const void* in[2];     // write: K and V
@@ -119,8 +119,17 @@ __device__ __forceinline__ bool grid_codes(const float (&x)[N], float lo, float 
   return true;
 }
 
+// CTAs that an SM holds at once (measured on 131072 tokens of 8 x 128 bf16, grids, and 16384 of
+// 32 x 128 fp16, blocks: reads 4 / 6 / 8 at once 130 / 124 / 143 us for grids, whose spills
+// start at 8, and 101 / 81 / 69 us for blocks), and the most rounds of rows of one
+template <int KIND>
+struct Resident {
+  static constexpr int WRITE = KIND == MX4 ? 5 : 3, READ = KIND == MX4 ? 8 : 6;
+};
+constexpr int ROUNDS = 32;
+
 template <typename T, int KIND>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, Resident<KIND>::WRITE)
 k_cache_write(const Args a, int32_t* status) {
   using U = Unit<T>;
   __shared__ Where stored[THREADS];
@@ -130,28 +139,24 @@ k_cache_write(const Args a, int32_t* status) {
   const int group = pl.lane >> a.lane_bits;
   const int first = pl.lane * U::N;                       // first value of the lane
   const int n = pl.live ? a.dim - first : 0;
-  const T* in = static_cast<const T*>(a.in[pl.kv]) + t0 * a.ldt[pl.kv] + pl.head * a.ldh[pl.kv] + first;
-  const int64_t ldt = a.ldt[pl.kv];
+  const T* in = static_cast<const T*>(a.in[pl.kv]) + (t0 + pl.row) * a.ldt[pl.kv] +
+                pl.head * a.ldh[pl.kv] + first;
+  const int64_t step = a.ldt[pl.kv] * a.side;
   uint32_t* codes0 = a.codes[pl.kv] + int64_t(pl.head) * a.words + first / (KIND == GRID8 ? 4 : 8);
   const int64_t group0 = int64_t(pl.head) * a.groups + group;
   bool bad = false;
-  // the next AHEAD rows are loading while a row is quantised (one copy of that code: unrolled
-  // over the rows it no longer fits the instruction cache)
-  U unit[AHEAD];
-#pragma unroll
-  for (int s = 0; s < AHEAD; ++s) {
-    const int r = s * a.side + pl.row;
-    unit[s].load(in + r * ldt, r < rows ? n : 0, a.vec != 0);
-  }
+  // the next row is loading while one is quantised (one copy of that code: unrolled over the
+  // rows it no longer fits the instruction cache; loading two ahead cost 6% for its registers)
+  U next;
+  next.load(in, pl.row < rows ? n : 0, a.vec != 0);
   if (int(threadIdx.x) < rows) stored[threadIdx.x] = find_row(a, t0 + threadIdx.x, status);
   __syncthreads();
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += a.side) {
-    const U now = unit[0];
-#pragma unroll
-    for (int s = 0; s + 1 < AHEAD; ++s) unit[s] = unit[s + 1];
-    const int r = r0 + pl.row, rn = r + AHEAD * a.side;
-    unit[AHEAD - 1].load(in + rn * ldt, rn < rows ? n : 0, a.vec != 0);
+    const U now = next;
+    const int r = r0 + pl.row;
+    in += step;
+    next.load(in, r + a.side < rows ? n : 0, a.vec != 0);
     {
       Where at = {-1, 0};
       if (r < rows && pl.live) at = stored[r];
@@ -219,7 +224,7 @@ k_cache_write(const Args a, int32_t* status) {
 }
 
 template <typename T, int KIND>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, Resident<KIND>::READ)
 k_cache_read(const Args a, int32_t* status) {
   using O = Out<T>;
   __shared__ Where stored[THREADS];
@@ -304,10 +309,15 @@ gptq_status launch(cudaStream_t st, bool write, Args& a, int32_t* status) {
   if (parts > 65535) return GPTQ_ERR_UNSUPPORTED;
   a.per_row = int(per_row);
   a.side = std::max(1, THREADS / a.per_row);
-  // rows of a CTA: enough to pay for finding their slots where that leaves eight CTAs per SM,
-  // and one row per thread at least
-  const int64_t want = a.tokens * parts / (8 * 148);
-  a.rows = int(std::min<int64_t>(THREADS, a.side * std::max<int64_t>(1, std::min<int64_t>(32, want / a.side))));
+  // rows of a CTA: as many as pay for finding their slots, in whole waves of resident CTAs
+  // (a last wave that was three quarters full cost 15%)
+  const int sms = sm_count();
+  if (sms <= 0) return GPTQ_ERR_CUDA;
+  const int64_t slots = int64_t(sms) * (write ? Resident<KIND>::WRITE : Resident<KIND>::READ);
+  const int64_t work = a.tokens * parts, most = std::min(THREADS / a.side, ROUNDS) * a.side;
+  const int64_t waves = (work + slots * most - 1) / (slots * most);
+  const int64_t even = (work + slots * waves - 1) / (slots * waves);
+  a.rows = int((even + a.side - 1) / a.side * a.side);
   const int64_t blocks = (a.tokens + a.rows - 1) / a.rows;
   const dim3 grid{unsigned(blocks), unsigned(parts)};
   if (write) GPTQ_LAUNCH((k_cache_write<T, KIND>), grid, THREADS, 0, st, a, status);
