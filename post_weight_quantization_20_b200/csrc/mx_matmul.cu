@@ -41,7 +41,7 @@ struct Prob {
   int boxes;         // boxes along K: 256 columns each
   uint32_t wait_limit;
   // k_mx_pair only
-  int bn;            // tokens of a tile, a multiple of 32
+  int bn;            // tokens of a tile, a multiple of 64
   int nb;            // scale tiles that a token tile touches
   int ntr, ntt;      // tiles along the layer rows and the tokens
 };
@@ -145,8 +145,6 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
     constexpr uint32_t idesc = idesc_of(128, BN);
     const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
     const uint64_t sdesc0 = tc::smem_desc_rows16(smem + C::SUB * (A_BOX + C::B_BOX));
-    // a token tile of 32 or 64 starts inside its scale tile, 32 rows to a TMEM column
-    const uint32_t first = uint32_t((n0 & 127) >> 5);
     for (int b = b0; b < b1; b += C::SUB) {
       ok = __all_sync(0xffffffffu, tc::mbar_wait(full + stage, phase, abort_flag, p.wait_limit));
       if (!ok) break;
@@ -172,7 +170,7 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
             tc::mma_mxf4(tmem_base, ad + (kk >> 2) * (A_BOX >> 4) + (kk & 3) * 2,
                          xd + (kk >> 2) * (C::B_BOX >> 4) + (kk & 3) * 2,
                          idesc | ((kk & 1) ? ODD_HALF : 0u), sfa + 4 * (kk >> 1),
-                         sfb + first + 4 * (kk >> 1), (b > b0 || kk > 0) ? 1u : 0u);
+                         sfb + 4 * (kk >> 1), (b > b0 || kk > 0) ? 1u : 0u);
         tc::mma_commit(empty + stage);
         if (b + C::SUB >= b1) tc::mma_commit(acc_full);
       }
@@ -264,13 +262,13 @@ namespace pair {
 
 constexpr int STAGES = 6;
 constexpr int BN = 256;                           // widest token tile
-constexpr int NB = 3;                             // scale tiles a token tile touches at most
+constexpr int NB = 2;                             // scale tiles a token tile touches at most
 constexpr int B_BYTES = BN / 2 * KB;              // 16 KB
 constexpr int STAGE = A_BOX + B_BYTES + 1024 * (1 + NB);
 constexpr int SF_COLS = 8 * (1 + NB);
 constexpr int SMEM = STAGES * STAGE + 1024 + 256;
 constexpr int THREADS = 320;
-constexpr int GROUP = 8;                          // token tiles per group of the tile order
+constexpr int GROUP = 16;                         // token tiles per group of the tile order
 static_assert(BN + STAGES * SF_COLS <= 512, "TMEM");
 
 // t-th tile: groups of GROUP token tiles, row tile by row tile inside a group, so that the
@@ -379,7 +377,9 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
       for (int t = pair_id; t < tiles && ok; t += n_pairs) {
         int r0, n0;
         tile_of(p, t, r0, n0);
-        const uint32_t first = uint32_t((n0 & 127) >> 5);
+        // a token tile may start in the middle of a scale tile, 32 tokens to a TMEM column; the
+        // MMA takes its scales from an even column only, so tiles are multiples of 64 tokens
+        const uint32_t first = uint32_t((n0 & 64) >> 5);
         if (!wait(acc_empty, acc_phase ^ 1u, true)) break;
         acc_phase ^= 1u;
         tc::fence_after_sync();
@@ -572,12 +572,12 @@ gptq_status by_tokens(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, u
   // 64 + bn/4 cycles (shared memory moves 4 KB of W and bn/64 KB of X in and out)
   int64_t best = 0;
   p.ntr = (p.R + 255) / 256;
-  for (int bn = 256; bn >= 64; bn -= 32) {
+  for (int bn = 256; bn >= 64; bn -= 64) {
     const int64_t tiles = int64_t(p.ntr) * ((p.M + bn - 1) / bn), pairs = sms / 2;
     const int64_t time = (tiles + pairs - 1) / pairs * (64 + bn / 4);
     if (best == 0 || time < best) { best = time; p.bn = bn; }
   }
-  p.nb = p.bn % 128 == 0 ? p.bn / 128 : (p.bn + 96 + 127) / 128;
+  p.nb = (p.bn + 127) / 128;      // 64 and 192 tokens start on either half of a scale tile
   p.ntt = (p.M + p.bn - 1) / p.bn;
   return launch_pair<T>(st, xc, wc, row_bytes, p, sms, status);
 }

@@ -152,7 +152,9 @@ def test_rows_past_32_bit_offsets():
 SHAPES = [(1, 128, 64), (1, 1, 1), (2, 130, 32), (1, 513, 4128), (3, 100, 96), (16, 128, 128),
           (17, 256, 300), (33, 70, 1000), (64, 384, 512), (65, 129, 2080), (127, 128, 257),
           (129, 300, 640), (256, 256, 1024), (300, 200, 4104), (257, 1000, 160), (700, 515, 1056),
-          (1, 4096, 12288), (5, 640, 20000), (520, 130, 8200)]
+          (1, 4096, 12288), (5, 640, 20000), (520, 130, 8200),
+          # every width of a token tile, tiles that start in the middle of 128 tokens among them
+          (256, 5120, 96), (384, 9472, 96), (500, 9472, 64), (700, 9472, 33)]
 
 
 @pytest.mark.parametrize("M,R,C", SHAPES)
