@@ -5,8 +5,8 @@
 // one or two shuffles), or writes 16 bytes read back; a warp's steps are loaded together.
 // Rows that are narrower than a warp's step share it, lanes_bits lanes to a row.
 // Rows that do not start on 16-byte boundaries are still read and written in whole 16-byte
-// granules, their bytes shifted into place: element by element they took 6 to 7 times as long
-// (20000 x 11003 bf16 read back: 609 us; through shared memory 236 us).
+// granules, their bytes or codes shifted into place: element by element they took 6 to 7 times
+// as long (20000 x 11003 bf16 read back: 609 us; through shared memory 236 us).
 #include <algorithm>
 
 #include "kernels.h"
@@ -31,18 +31,15 @@ template <int N, int STEPS, bool WIDE>
 struct Item {
   int64_t row0;
   int col0, step;     // of step 0; rows (narrow) or columns (wide) per step
-  bool first;         // the lane holds the first columns of its row in a step
   __device__ Item(const Walk& w, int64_t item, int lane) {
     if (WIDE) {
       row0 = item / w.spans;
       col0 = int(item - row0 * w.spans) * (STEPS * 32 * N) + lane * N;
       step = 32 * N;
-      first = lane == 0;
     } else {
       step = 32 >> w.lane_bits;
       row0 = item * (STEPS * step) + (lane >> w.lane_bits);
       col0 = (lane & ((1 << w.lane_bits) - 1)) * N;
-      first = col0 == 0;
     }
   }
   __device__ __forceinline__ int64_t row(int s) const { return WIDE ? row0 : row0 + s * step; }
@@ -108,6 +105,9 @@ k_mx_quantize(const T* __restrict__ X, int64_t ldx, const Walk w, uint32_t* __re
   if (bad) raise_status(status, GPTQ_ERR_NONFINITE);
 }
 
+// VEC: every row of Y starts on a 16-byte boundary.  Otherwise the lanes' units are moved back
+// within each row to the boundaries there are: a unit then starts `shift` columns earlier, its
+// codes straddle two words and perhaps two blocks, and its store is whole all the same.
 template <typename T, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(WARPS * 32)
 k_mx_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, const Walk w,
@@ -119,29 +119,55 @@ k_mx_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ 
   if (item >= w.items) return;
   const Item<O::N, STEPS, WIDE> it(w, item, lane);
   const int nb = (w.cols + 31) >> 5, ct = (nb + 3) >> 2;
-  uint32_t q[STEPS], e[STEPS];
+  uint32_t q[STEPS], q1[VEC ? 1 : STEPS], e[STEPS], e1[VEC ? 1 : STEPS];
+  const auto shift = [&](int64_t row) {
+    return VEC ? 0 : int(reinterpret_cast<uintptr_t>(Y + row * ldy) & 15) / int(sizeof(T));
+  };
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int64_t row = it.row(s);
-    const int c = it.col(s);
+    const int c = it.col(s) - shift(row);
     q[s] = e[s] = 0;
-    if ((WIDE || row < w.rows) && c < w.cols) {
-      q[s] = __ldg(codes + row * (4 * int64_t(nb)) + (c >> 3));
-      e[s] = __ldg(scales + mx::scale_offset(row, c >> 5, ct));
+    if constexpr (!VEC) q1[s] = e1[s] = 0;
+    if (WIDE || row < w.rows) {
+      const uint32_t* p = codes + row * (4 * int64_t(nb));
+      if (VEC) {
+        if (c < w.cols) {
+          q[s] = __ldg(p + (c >> 3));
+          e[s] = __ldg(scales + mx::scale_offset(row, c >> 5, ct));
+        }
+      } else {
+        const int last = c + O::N - 1;
+        if (c >= 0 && c < w.cols) {
+          q[s] = __ldg(p + (c >> 3));
+          e[s] = __ldg(scales + mx::scale_offset(row, c >> 5, ct));
+        }
+        if (last >= 0 && last < 32 * nb) {
+          q1[s] = __ldg(p + (last >> 3));
+          e1[s] = __ldg(scales + mx::scale_offset(row, last >> 5, ct));
+        }
+      }
     }
   }
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int64_t row = it.row(s);
-    const int c = it.col(s), n = WIDE || row < w.rows ? w.cols - c : 0;
+    const int c = it.col(s) - shift(row);
     float v[O::N];
-    mx::decode<O::N>(O::N == 4 ? q[s] >> (4 * (c & 4)) : q[s], v);
+    uint32_t w0 = q[s];
+    // the unit's codes as the lowest bits of one word
+    if constexpr (!VEC) w0 = __funnelshift_r(q[s], q1[s], 4 * (c & 7));
+    else if (O::N == 4) w0 >>= 4 * (c & 4);
+    mx::decode<O::N>(w0, v);
     const float f = mx::scale_value(e[s]);
+    const float f1 = VEC ? f : mx::scale_value(e1[VEC ? 0 : s]);
+    const int own = 32 - (c & 31);                      // elements of the unit's first block
 #pragma unroll
-    for (int i = 0; i < O::N; ++i) v[i] *= f;
+    for (int i = 0; i < O::N; ++i) v[i] *= VEC || i < own ? f : f1;
     T* p = Y + row * ldy + c;
+    const int n = WIDE || row < w.rows ? w.cols - c : 0;
     if constexpr (VEC) O::store(p, n, true, v);
-    else O::store_any(p, n, !it.first, v);
+    else O::store_some(p, -c, n, v);
   }
 }
 
@@ -151,16 +177,17 @@ bool rows_aligned(const void* p, int64_t ld, int64_t rows) {
   return ((reinterpret_cast<uintptr_t>(p) | (rows > 1 ? uintptr_t(ld) * sizeof(T) : 0)) & 15) == 0;
 }
 
-// `least`: lane_bits of the narrowest row (4 blocks, whose scales are stored together)
-Walk walk_of(int64_t rows, int cols, int n, int steps, int least) {
+// `reach`: columns of a row that the lanes have to cover; `least`: lane_bits of the narrowest
+// row (4 blocks, whose scales are stored together)
+Walk walk_of(int64_t rows, int cols, int reach, int n, int steps, int least) {
   Walk w{rows, cols, 5, 1, 0};
-  const int lanes = ((cols + 31) / 32 * 32 + n - 1) / n;
+  const int lanes = ((reach + 31) / 32 * 32 + n - 1) / n;
   if (lanes <= 16) {
     w.lane_bits = least;
     while ((1 << w.lane_bits) < lanes) ++w.lane_bits;
   }
   if (w.lane_bits == 5) {
-    w.spans = int((int64_t(cols) + steps * 32 * n - 1) / (steps * 32 * n));
+    w.spans = int((int64_t(reach) + steps * 32 * n - 1) / (steps * 32 * n));
     w.items = rows * w.spans;
   } else {
     const int64_t per = int64_t(steps) << (5 - w.lane_bits);
@@ -194,7 +221,7 @@ gptq_status dequantize_v(cudaStream_t st, const uint32_t* codes, const uint8_t* 
 template <typename T>
 gptq_status quantize_t(cudaStream_t st, const void* X, int64_t rows, int cols, int64_t ldx,
                        uint32_t* codes, uint8_t* scales, int32_t* status) {
-  const Walk w = walk_of(rows, cols, Unit<T>::N, sizeof(T) == 4 ? 4 : 2, sizeof(T) == 4 ? 4 : 3);
+  const Walk w = walk_of(rows, cols, cols, Unit<T>::N, sizeof(T) == 4 ? 4 : 2, sizeof(T) == 4 ? 4 : 3);
   const T* x = static_cast<const T*>(X);
   return rows_aligned<T>(X, ldx, rows) ? quantize_v<T, true>(st, x, ldx, w, codes, scales, status)
                                        : quantize_v<T, false>(st, x, ldx, w, codes, scales, status);
@@ -203,17 +230,18 @@ gptq_status quantize_t(cudaStream_t st, const void* X, int64_t rows, int cols, i
 template <typename T>
 gptq_status dequantize_t(cudaStream_t st, const uint32_t* codes, const uint8_t* scales,
                          int64_t rows, int cols, void* Y, int64_t ldy) {
-  const Walk w = walk_of(rows, cols, Out<T>::N, 4, 0);
   T* y = static_cast<T*>(Y);
-  return rows_aligned<T>(Y, ldy, rows) ? dequantize_v<T, true>(st, codes, scales, w, y, ldy)
-                                       : dequantize_v<T, false>(st, codes, scales, w, y, ldy);
+  if (rows_aligned<T>(Y, ldy, rows))
+    return dequantize_v<T, true>(st, codes, scales, walk_of(rows, cols, cols, Out<T>::N, 4, 0), y, ldy);
+  const int wide = cols + Out<T>::N - 1;               // moved back by up to N - 1 columns
+  return dequantize_v<T, false>(st, codes, scales, walk_of(rows, cols, wide, Out<T>::N, 4, 0), y, ldy);
 }
 
 }  // namespace
 
 // an item is never less than 512 elements of one row, or a row
 bool mx_grid_fits(int64_t rows, int64_t cols) {
-  return rows * ((cols + 511) / 512) <= (int64_t(1) << 31) * WARPS - WARPS;
+  return rows * ((cols + 518) / 512) <= (int64_t(1) << 31) * WARPS - WARPS;
 }
 
 gptq_status mx_quantize_run(cudaStream_t st, const void* X, int dt, int64_t rows, int cols,

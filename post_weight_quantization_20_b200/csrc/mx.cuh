@@ -245,31 +245,15 @@ struct Out {
       return make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  // The same to any address, by a whole warp whose lanes hold consecutive units: a lane writes
-  // the 16-byte granule in which its unit starts, the first bytes of it from the lane before
-  // (`prev`: there is one, in the same row), and single elements where a granule is not whole.
-  static __device__ __forceinline__ void store_any(T* p, int n, bool prev, const float (&v)[N]) {
-    const uint4 d = pack(v);
-    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
-    const int ae = int(off) / int(sizeof(T));          // elements of the next lane's granule
-    uint32_t w[9] = {__shfl_up_sync(0xffffffffu, d.x, 1), __shfl_up_sync(0xffffffffu, d.y, 1),
-                     __shfl_up_sync(0xffffffffu, d.z, 1), __shfl_up_sync(0xffffffffu, d.w, 1),
-                     d.x, d.y, d.z, d.w, 0u};
-    const bool whole = prev && n >= N - ae;
-    const int next = __shfl_down_sync(0xffffffffu, int(whole), 1);
-    const bool next_whole = (threadIdx.x & 31) != 31 && next != 0;
-    if (whole) {
-      if (off == 0) {
-        *reinterpret_cast<uint4*>(p) = d;
-      } else {
-        Unit<T>::template shift_words<9>(w, 16u - off);
-        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(p) - off) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-    if (!whole || !next_whole) {
+  // Elements from .. n-1 of the unit: the whole of it at once, which p's 16 bytes must be
+  // aligned for, or one by one.
+  static __device__ __forceinline__ void store_some(T* p, int from, int n, const float (&v)[N]) {
+    if (from <= 0 && n >= N) {
+      *reinterpret_cast<uint4*>(p) = pack(v);
+    } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (i < n && !(i < N - ae ? whole : next_whole)) p[i] = from_f32<T>(v[i]);
+        if (i >= from && i < n) p[i] = from_f32<T>(v[i]);
     }
   }
   // `n` elements exist; vec: p is a multiple of 16 bytes
