@@ -43,6 +43,7 @@ struct Prob {
   // k_mx_pair only
   int bn;            // tokens of a tile, a multiple of 64
   int nb;            // scale tiles that a token tile touches
+  int accs;          // accumulators
   int ntr, ntt;      // tiles along the layer rows and the tokens
 };
 
@@ -93,6 +94,10 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
   const int b0 = int(int64_t(p.boxes) * split / splits);
   const int b1 = int(int64_t(p.boxes) * (split + 1) / splits);
 
+  if (threadIdx.x == 32) {
+    tc::prefetch_map(&wmap);
+    tc::prefetch_map(&xmap);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       tc::mbar_init(full + i, 1);
@@ -256,11 +261,12 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
 // and tokens n0 + bn/2 r .. (its halves of the operands), the scales of its layer rows and of
 // all of the tile's tokens; rank 0 issues the MMAs.  The accumulator rows r0 + 128 r .. land
 // in rank r's TMEM.  8 epilogue warps per CTA take the whole tile into registers and release
-// the accumulator before they convert and store, so that the next tile's MMAs run meanwhile
-// (two accumulators of 256 tokens and the scales do not fit the 512 TMEM columns).
+// the accumulator before they convert and store.  Up to 192 tokens two accumulators alternate,
+// so that the next tile's MMAs do not wait for that; two of 256 tokens and the scales do not
+// fit the 512 TMEM columns, and each tile then starts about 2000 cycles after the last.
 namespace pair {
 
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int BN = 256;                           // widest token tile
 constexpr int NB = 2;                             // scale tiles a token tile touches at most
 constexpr int B_BYTES = BN / 2 * KB;              // 16 KB
@@ -269,7 +275,8 @@ constexpr int SF_COLS = 8 * (1 + NB);
 constexpr int SMEM = STAGES * STAGE + 1024 + 256;
 constexpr int THREADS = 320;
 constexpr int GROUP = 16;                         // token tiles per group of the tile order
-static_assert(BN + STAGES * SF_COLS <= 512, "TMEM");
+constexpr int SF_BASE = 512 - STAGES * SF_COLS;   // TMEM columns below: accumulators
+static_assert(BN <= SF_BASE && 2 * 192 <= SF_BASE, "TMEM");
 
 // t-th tile: groups of GROUP token tiles, row tile by row tile inside a group, so that the
 // tiles in flight together share operand rows in L2
@@ -292,8 +299,8 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drain = acc_empty + 1;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* issued_slot = tmem_slot + 2;          // the partner's fill count (abort path)
@@ -305,13 +312,21 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   // bytes of one fill, both CTAs' loads (boxes past the tensors' ends count in full)
   const uint32_t fill = 2 * uint32_t(A_BOX + p.bn / 2 * KB + 1024 * (1 + p.nb));
 
+  if (threadIdx.x == 64) {
+    tc::prefetch_map(&wmap);
+    tc::prefetch_map(&xmap);
+    tc::prefetch_map(&wsmap);
+    tc::prefetch_map(&xsmap);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       tc::mbar_init(full + i, 1);
       tc::mbar_init(empty + i, 1);
     }
-    tc::mbar_init(acc_full, 1);
-    tc::mbar_init(acc_empty, 16);                 // 8 epilogue warps of each CTA
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(acc_full + i, 1);
+      tc::mbar_init(acc_empty + i, 16);           // 8 epilogue warps of each CTA
+    }
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
     *issued_slot = 0;
@@ -371,6 +386,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     if (rank == 0) {
       int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
+      int acc = 0;
       bool ok = true;
       const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
       const uint64_t sdesc0 = tc::smem_desc_rows16(smem + A_BOX + B_BYTES);
@@ -380,8 +396,8 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         // a token tile may start in the middle of a scale tile, 32 tokens to a TMEM column; the
         // MMA takes its scales from an even column only, so tiles are multiples of 64 tokens
         const uint32_t first = uint32_t((n0 & 64) >> 5);
-        if (!wait(acc_empty, acc_phase ^ 1u, true)) break;
-        acc_phase ^= 1u;
+        if (!wait(acc_empty + acc, acc_phase ^ 1u, true)) break;
+        const uint32_t d = tmem_base + uint32_t(acc * p.bn);
         tc::fence_after_sync();
         for (int b = 0; b < p.boxes; ++b) {
           if (!wait(full + stage, phase)) { ok = false; break; }
@@ -390,7 +406,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
           const uint64_t ad = adesc0 + uint32_t(stage) * (STAGE >> 4);
           const uint64_t xd = ad + (A_BOX >> 4);
           const uint64_t sd = sdesc0 + uint32_t(stage) * (STAGE >> 4);
-          const uint32_t sfa = tmem_base + uint32_t(BN + stage * SF_COLS);
+          const uint32_t sfa = tmem_base + uint32_t(SF_BASE + stage * SF_COLS);
           const uint32_t sfb = sfa + 8, half = 4 * uint32_t(p.nb);
           const int todo = p.steps - 4 * b;
           if (tc::elect_one()) {
@@ -404,40 +420,42 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               if (kk < todo)
-                tc::mma_mxf4_pair(tmem_base, ad + 2 * kk, xd + 2 * kk,
+                tc::mma_mxf4_pair(d, ad + 2 * kk, xd + 2 * kk,
                                   idesc | ((kk & 1) ? ODD_HALF : 0u), sfa + 4 * (kk >> 1),
                                   sfb + first + half * (kk >> 1), (b > 0 || kk > 0) ? 1u : 0u);
             tc::mma_commit_pair(empty + stage, 0x3);
-            if (b + 1 == p.boxes) tc::mma_commit_pair(acc_full, 0x3);
+            if (b + 1 == p.boxes) tc::mma_commit_pair(acc_full + acc, 0x3);
           }
           __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
+        if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
       }
     }
   } else {
     const int lane_base = (warp & 3) * 32;
-    const int c0 = ((warp - 2) >> 2) * 128;       // this warp's tokens of the tile
+    const int half = p.bn / 2, c0 = ((warp - 2) >> 2) * half;     // this warp's tokens of the tile
     const uint32_t acc_empty0 = tc::cluster_addr(acc_empty, 0);
     uint32_t acc_phase = 0;
+    int acc = 0;
     for (int t = pair_id; t < tiles; t += n_pairs) {
       int r0, n0;
       tile_of(p, t, r0, n0);
-      if (!tc::mbar_wait_pair(acc_full, acc_phase, abort_flag, peer_flag, p.wait_limit)) break;
-      acc_phase ^= 1u;
+      if (!tc::mbar_wait_pair(acc_full + acc, acc_phase, abort_flag, peer_flag, p.wait_limit)) break;
       tc::fence_after_sync();
       uint32_t v[4][32];
-      const uint32_t at = tmem_base + (uint32_t(lane_base) << 16) + uint32_t(c0);
+      const uint32_t at = tmem_base + (uint32_t(lane_base) << 16) + uint32_t(acc * p.bn + c0);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (c0 + 32 * c < p.bn) tc::tmem_ld_32x32(at + 32 * c, v[c]);
+        if (32 * c < half) tc::tmem_ld_32x32(at + 32 * c, v[c]);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(acc_empty0);
+      if (lane == 0) tc::mbar_arrive_cluster(acc_empty0 + uint32_t(acc * 8));
+      if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
       const int row = r0 + 128 * int(rank) + lane_base + lane;
       if (row < p.R) {
-        const int live = min(p.bn, p.M - n0) - c0;
+        const int live = min(half, p.M - n0 - c0);
         T* y = static_cast<T*>(p.Y) + int64_t(n0 + c0) * p.ldy + row;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -568,15 +586,17 @@ gptq_status by_tokens(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, u
   if (p.M <= 32) return launch_few<32, T>(st, xc, wc, row_bytes, p, sms, status);
   if (p.M <= 64) return launch_few<64, T>(st, xc, wc, row_bytes, p, sms, status);
   if (p.M <= 128) return launch_few<128, T>(st, xc, wc, row_bytes, p, sms, status);
-  // the widest token tile by the time of the pairs' waves: a tile's step takes about
-  // 64 + bn/4 cycles (shared memory moves 4 KB of W and bn/64 KB of X in and out)
+  // the widest token tile by the time of the pairs' waves, in cycles: a step takes about
+  // 64 + bn/4 (shared memory moves 4 KB of W and bn/64 KB of X in and out), a tile of a single
+  // accumulator starts late
   int64_t best = 0;
   p.ntr = (p.R + 255) / 256;
   for (int bn = 256; bn >= 64; bn -= 64) {
     const int64_t tiles = int64_t(p.ntr) * ((p.M + bn - 1) / bn), pairs = sms / 2;
-    const int64_t time = (tiles + pairs - 1) / pairs * (64 + bn / 4);
+    const int64_t time = (tiles + pairs - 1) / pairs * (int64_t(p.steps) * (64 + bn / 4) + (bn > 192 ? 2000 : 200));
     if (best == 0 || time < best) { best = time; p.bn = bn; }
   }
+  p.accs = p.bn > 192 ? 1 : 2;
   p.nb = (p.bn + 127) / 128;      // 64 and 192 tokens start on either half of a scale tile
   p.ntt = (p.M + p.bn - 1) / p.bn;
   return launch_pair<T>(st, xc, wc, row_bytes, p, sms, status);

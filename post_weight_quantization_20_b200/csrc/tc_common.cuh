@@ -94,6 +94,11 @@ __device__ __forceinline__ void drain_tma_ring(uint64_t* full, int stages, int64
   }
 }
 
+// Fetch a kernel parameter's tensor map ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
   asm volatile(
