@@ -235,7 +235,7 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
         if (row + i < p.R) y[i] = from_f32<T>(o[i]);
     }
     __syncwarp();
-    tc::cluster_sync();                // no CTA leaves while its partial sums are read
+    tc::cluster_sync_relaxed();        // no CTA leaves while its partial sums are read
   }
   if (*abort_flag) {
     if (warp == 0 && lane == 0) tc::drain_tma_ring(full, C::STAGES, issued);
@@ -451,25 +451,34 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(acc_empty0 + uint32_t(acc * 8));
+      if (lane == 0) tc::mbar_arrive_cluster_relaxed(acc_empty0 + uint32_t(acc * 8));
       if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
       const int row = r0 + 128 * int(rank) + lane_base + lane;
       if (row < p.R) {
         const int live = min(half, p.M - n0 - c0);
         T* y = static_cast<T*>(p.Y) + int64_t(n0 + c0) * p.ldy + row;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          if (32 * c + 32 <= live) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (32 * c + i < live) *y = from_f32<T>(__uint_as_float(v[c][i]));
-            y += p.ldy;
+            for (int i = 0; i < 32; ++i) {
+              *y = from_f32<T>(__uint_as_float(v[c][i]));
+              y += p.ldy;
+            }
+          } else if (32 * c < live) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (32 * c + i < live) *y = from_f32<T>(__uint_as_float(v[c][i]));
+              y += p.ldy;
+            }
           }
+        }
       }
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  tc::cluster_sync();          // both CTAs out of their loops: the abort flags are final
+  tc::cluster_sync_relaxed();  // both CTAs out of their loops: the abort flags are final
   if (*abort_flag) {
     // A wait gave up in one of the CTAs, which raised both flags.  (1) rank 0's MMAs land;
     // (2) the producers exchange their fill counts and the one behind fills the phases the

@@ -285,6 +285,13 @@ __device__ __forceinline__ void cluster_sync() {
                    "memory");
 }
 
+// The same as an execution barrier only: earlier writes of the CTAs are not made visible (nor
+// waited for: a release waits until every global store before it has been performed, about
+// 1000 cycles behind an epilogue).
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void st_cluster_u32(uint32_t caddr, uint32_t v) {
   asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
 }
@@ -308,6 +315,12 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t caddr) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr)
                : "memory");
+}
+
+// The same without a release, for an arrival that hands over TMEM and no memory: the waiting
+// side is ordered by the tcgen05 fences around the arrival and the wait.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
@@ -334,6 +347,7 @@ __device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, v
   }
   *abort_flag = 1;
   st_cluster_u32(peer_flag, 1u);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");   // before any later cluster barrier
   return false;
 }
 
