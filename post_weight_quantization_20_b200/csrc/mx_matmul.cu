@@ -10,7 +10,7 @@
 // after the MMAs that read them have released the stage.
 //
 // Two kernels:
-//  k_mx_few    128 layer rows x up to 128 tokens per CTA, K split over the CTAs of a cluster,
+//  k_mx_few    128 layer rows x up to 64 tokens per CTA, K split over the CTAs of a cluster,
 //              whose partial sums meet in distributed shared memory in a fixed order: few
 //              tokens, where the weights' bytes are the work and row tiles alone would leave
 //              SMs idle.
@@ -44,6 +44,7 @@ struct Prob {
   int bn;            // tokens of a tile, a multiple of 64
   int nb;            // scale tiles that a token tile touches
   int accs;          // accumulators
+  int stages;        // of the ring
   int ntr, ntt;      // tiles along the layer rows and the tokens
 };
 
@@ -60,7 +61,7 @@ constexpr int FEW_THREADS = 192;        // warp 0 producer, warp 1 TMEM and MMA,
 
 template <int BN>
 struct Few {
-  static constexpr int SUB = BN <= 64 ? 2 : 1;                // boxes of a stage
+  static constexpr int SUB = 2;                               // boxes of a stage
   static constexpr int B_BOX = BN * KB;
   static constexpr int S_BOX = 1024;                          // scales of 128 rows and a box
   static constexpr int STAGE = SUB * (A_BOX + B_BOX + 2 * S_BOX);
@@ -261,22 +262,38 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
 // and tokens n0 + bn/2 r .. (its halves of the operands), the scales of its layer rows and of
 // all of the tile's tokens; rank 0 issues the MMAs.  The accumulator rows r0 + 128 r .. land
 // in rank r's TMEM.  8 epilogue warps per CTA take the whole tile into registers and release
-// the accumulator before they convert and store.  Up to 192 tokens two accumulators alternate,
-// so that the next tile's MMAs do not wait for that; two of 256 tokens and the scales do not
-// fit the 512 TMEM columns, and each tile then starts about 2000 cycles after the last.
+// the accumulator before they convert and store.  Up to 128 tokens two accumulators alternate,
+// so that the next tile's MMAs do not wait for that; two of more and the scales do not fit the
+// 512 TMEM columns, and each tile then starts about 2000 cycles after the last.
 namespace pair {
 
-constexpr int STAGES = 5;
-constexpr int BN = 256;                           // widest token tile
-constexpr int NB = 2;                             // scale tiles a token tile touches at most
-constexpr int B_BYTES = BN / 2 * KB;              // 16 KB
-constexpr int STAGE = A_BOX + B_BYTES + 1024 * (1 + NB);
-constexpr int SF_COLS = 8 * (1 + NB);
-constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+// A stage of the ring is two boxes, 512 columns: each stage costs the issuing warp about 400
+// cycles of waiting, committing and looping whatever it holds, which one box's MMAs hide at 256
+// tokens only (256 cycles at 128 tokens).  The ring's shape goes with the token tile.
+constexpr int SUB = 2;                            // boxes of a stage
+constexpr int MAX_STAGES = 5;
+constexpr int RING = 222 * 1024;                  // bytes of shared memory for the stages
+constexpr int SMEM = RING + 1024 /*align*/ + 256 /*barriers*/;
+constexpr int NB = 2;                             // scale tiles that a token tile touches at most
 constexpr int THREADS = 320;
 constexpr int GROUP = 16;                         // token tiles per group of the tile order
-constexpr int SF_BASE = 512 - STAGES * SF_COLS;   // TMEM columns below: accumulators
-static_assert(BN <= SF_BASE && 2 * 192 <= SF_BASE, "TMEM");
+
+// Byte offsets in a stage: W's boxes first, then X's, then the scales of W and of X.
+__host__ __device__ constexpr int x_off() { return SUB * A_BOX; }
+__host__ __device__ constexpr int s_off(int bn) { return x_off() + SUB * (bn / 2) * KB; }
+__host__ __device__ constexpr int stage_bytes(int bn, int nb) { return s_off(bn) + SUB * 1024 * (1 + nb); }
+__host__ __device__ constexpr int sf_cols(int nb) { return SUB * 8 * (1 + nb); }
+__host__ __device__ constexpr int tile_nb(int bn) { return (bn + 127) / 128; }   // 64 and 192 tokens
+                                                  // start on either half of a scale tile
+__host__ __device__ constexpr int stages_of(int bn) {
+  return RING / stage_bytes(bn, tile_nb(bn)) < MAX_STAGES ? RING / stage_bytes(bn, tile_nb(bn)) : MAX_STAGES;
+}
+__host__ __device__ constexpr int accs_of(int bn) { return bn <= 128 ? 2 : 1; }
+constexpr bool fits(int bn) {
+  return accs_of(bn) * bn + stages_of(bn) * sf_cols(tile_nb(bn)) <= 512 && stages_of(bn) >= 3 &&
+         stage_bytes(bn, tile_nb(bn)) % 1024 == 0;
+}
+static_assert(fits(64) && fits(128) && fits(192) && fits(256), "TMEM, shared memory");
 
 // t-th tile: groups of GROUP token tiles, row tile by row tile inside a group, so that the
 // tiles in flight together share operand rows in L2
@@ -296,9 +313,9 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE);
-  uint64_t* empty = full + STAGES;
-  uint64_t* acc_full = empty + STAGES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING);
+  uint64_t* empty = full + MAX_STAGES;
+  uint64_t* acc_full = empty + MAX_STAGES;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -309,8 +326,9 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   const uint32_t rank = tc::cluster_rank();
   const int pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int tiles = p.ntr * p.ntt;
-  // bytes of one fill, both CTAs' loads (boxes past the tensors' ends count in full)
-  const uint32_t fill = 2 * uint32_t(A_BOX + p.bn / 2 * KB + 1024 * (1 + p.nb));
+  const int nk = (p.boxes + SUB - 1) / SUB;       // stages of a tile
+  const int stages = p.stages, bytes = stage_bytes(p.bn, p.nb), cols = sf_cols(p.nb);
+  const uint32_t sf_base = 512 - uint32_t(stages * cols);      // TMEM columns below: accumulators
 
   if (threadIdx.x == 64) {
     tc::prefetch_map(&wmap);
@@ -319,7 +337,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     tc::prefetch_map(&xsmap);
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < MAX_STAGES; ++i) {
       tc::mbar_init(full + i, 1);
       tc::mbar_init(empty + i, 1);
     }
@@ -343,18 +361,22 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   const uint32_t peer_flag = tc::cluster_addr(const_cast<int*>(abort_flag), rank ^ 1u);
   int64_t issued = 0;
 
-  const auto load = [&](int stage, int b, int r0, int n0) {
-    uint8_t* a = smem + stage * STAGE;
-    uint8_t* x = a + A_BOX;
-    uint8_t* s = x + B_BYTES;
-    if (rank == 0) tc::mbar_expect_tx(full + stage, fill);
+  // one fill: boxes past the tensors' ends read as zeros and count in full
+  const auto load = [&](int stage, int k, int r0, int n0) {
+    uint8_t* a = smem + stage * bytes;
+    uint8_t* x = a + x_off();
+    uint8_t* s = a + s_off(p.bn);
+    if (rank == 0) tc::mbar_expect_tx(full + stage, 2 * uint32_t(bytes));
     const uint32_t cbar = tc::cluster_addr(full + stage, 0);
-    tc::tma_load_2d_pair(a, &wmap, b * KB, r0 + 128 * int(rank), cbar);
-    tc::tma_load_2d_pair(x, &xmap, b * KB, n0 + p.bn / 2 * int(rank), cbar);
-    tc::tma_load_2d_pair(s, &wsmap, b * 256, r0 / 128 + int(rank), cbar);
-    tc::tma_load_2d_pair(s + 1024, &xsmap, b * 256, n0 / 128, cbar);
+    const int ra = r0 + 128 * int(rank), rx = n0 + p.bn / 2 * int(rank);
+#pragma unroll
+    for (int j = 0; j < SUB; ++j) {
+      tc::tma_load_2d_pair(a + j * A_BOX, &wmap, (SUB * k + j) * KB, ra, cbar);
+      tc::tma_load_2d_pair(x + j * (p.bn / 2 * KB), &xmap, (SUB * k + j) * KB, rx, cbar);
+    }
+    tc::tma_load_2d_pair(s, &wsmap, k * 256, r0 / 128 + int(rank), cbar);
+    tc::tma_load_2d_pair(s + SUB * 1024, &xsmap, k * 256, n0 / 128, cbar);
   };
-
   const auto wait = [&](uint64_t* bar, uint32_t parity, bool cluster_scope = false) {
     return __all_sync(0xffffffffu, tc::mbar_wait_pair(bar, parity, abort_flag, peer_flag, p.wait_limit,
                                                       cluster_scope));
@@ -367,19 +389,19 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     for (int t = pair_id; t < tiles && ok; t += n_pairs) {
       int r0, n0;
       tile_of(p, t, r0, n0);
-      for (int b = 0; b < p.boxes; ++b) {
+      for (int k = 0; k < nk; ++k) {
         if (!wait(empty + stage, phase ^ 1u)) { ok = false; break; }
-        if (tc::elect_one()) load(stage, b, r0, n0);
+        if (tc::elect_one()) load(stage, k, r0, n0);
         __syncwarp();
         ++issued;
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
     }
     // every fill consumed: the MMAs' last arrivals on this CTA's empty barriers have landed
     // before the CTA can exit
     if (ok)
-      for (int st = 0; st < STAGES; ++st) {
-        const int64_t n = issued / STAGES + (st < issued % STAGES ? 1 : 0);
+      for (int st = 0; st < stages; ++st) {
+        const int64_t n = issued / stages + (st < issued % stages ? 1 : 0);
         if (n > 0 && !wait(empty + st, uint32_t((n - 1) & 1))) break;
       }
   } else if (warp == 1) {
@@ -389,7 +411,9 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
       int acc = 0;
       bool ok = true;
       const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
-      const uint64_t sdesc0 = tc::smem_desc_rows16(smem + A_BOX + B_BYTES);
+      const uint64_t sdesc0 = tc::smem_desc_rows16(smem + s_off(p.bn));
+      const uint32_t xbox = uint32_t(p.bn / 2 * KB) >> 4;       // descriptors count in 16 bytes
+      const uint32_t tile_cols = 4 * uint32_t(p.nb);            // TMEM columns of 128 columns' scales of X
       for (int t = pair_id; t < tiles && ok; t += n_pairs) {
         int r0, n0;
         tile_of(p, t, r0, n0);
@@ -399,35 +423,36 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         if (!wait(acc_empty + acc, acc_phase ^ 1u, true)) break;
         const uint32_t d = tmem_base + uint32_t(acc * p.bn);
         tc::fence_after_sync();
-        for (int b = 0; b < p.boxes; ++b) {
+        for (int k = 0; k < nk; ++k) {
           if (!wait(full + stage, phase)) { ok = false; break; }
           tc::fence_after_sync();
-          // descriptors count in 16 bytes
-          const uint64_t ad = adesc0 + uint32_t(stage) * (STAGE >> 4);
-          const uint64_t xd = ad + (A_BOX >> 4);
-          const uint64_t sd = sdesc0 + uint32_t(stage) * (STAGE >> 4);
-          const uint32_t sfa = tmem_base + uint32_t(SF_BASE + stage * SF_COLS);
-          const uint32_t sfb = sfa + 8, half = 4 * uint32_t(p.nb);
-          const int todo = p.steps - 4 * b;
+          const uint64_t ad = adesc0 + uint32_t(stage * (bytes >> 4));
+          const uint64_t xd = ad + (x_off() >> 4);
+          const uint64_t sd = sdesc0 + uint32_t(stage * (bytes >> 4));
+          const uint32_t sfa = tmem_base + sf_base + uint32_t(stage * cols);
+          const uint32_t sfb = sfa + 8 * SUB;
+          const int todo = p.steps - 4 * SUB * k;
           if (tc::elect_one()) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2 * SUB; ++h) {
               tc::copy_scales_pair(sfa + 4 * h, sd + 32 * h);
 #pragma unroll
               for (int j = 0; j < NB; ++j)
-                if (j < p.nb) tc::copy_scales_pair(sfb + half * h + 4 * j, sd + 64 * (1 + j) + 32 * h);
+                if (j < p.nb)
+                  tc::copy_scales_pair(sfb + tile_cols * h + 4 * j, sd + 64 * SUB * (1 + j) + 32 * h);
             }
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
+            for (int kk = 0; kk < 4 * SUB; ++kk)
               if (kk < todo)
-                tc::mma_mxf4_pair(d, ad + 2 * kk, xd + 2 * kk,
+                tc::mma_mxf4_pair(d, ad + (kk >> 2) * (A_BOX >> 4) + 2 * (kk & 3),
+                                  xd + (kk >> 2) * xbox + 2 * (kk & 3),
                                   idesc | ((kk & 1) ? ODD_HALF : 0u), sfa + 4 * (kk >> 1),
-                                  sfb + first + half * (kk >> 1), (b > 0 || kk > 0) ? 1u : 0u);
+                                  sfb + first + tile_cols * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
             tc::mma_commit_pair(empty + stage, 0x3);
-            if (b + 1 == p.boxes) tc::mma_commit_pair(acc_full + acc, 0x3);
+            if (k + 1 == nk) tc::mma_commit_pair(acc_full + acc, 0x3);
           }
           __syncwarp();
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
         if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
       }
@@ -498,8 +523,8 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     tc::cluster_sync();
     if (warp == 0 && lane == 0) {
       const int64_t other = int64_t(*issued_slot);
-      for (int64_t f = issued; f < other; ++f) load(int(f % STAGES), 0, 0, 0);
-      if (rank == 0) tc::drain_tma_ring(full, STAGES, other > issued ? other : issued);
+      for (int64_t f = issued; f < other; ++f) load(int(f % stages), 0, 0, 0);
+      if (rank == 0) tc::drain_tma_ring(full, stages, other > issued ? other : issued);
     }
     tc::fence_before_sync();
     tc::cluster_sync();
@@ -528,17 +553,17 @@ bool encode_codes(CUtensorMap* m, const uint32_t* codes, uint64_t row_bytes, uin
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// scale tiles as rows (128 matrix rows) of ct * 512 bytes, boxes of two tiles x box_rows;
+// scale tiles as rows (128 matrix rows) of ct * 512 bytes, boxes of four tiles x box_rows;
 // tiles past the ends read as zeros
 bool encode_scales(CUtensorMap* m, const uint8_t* scales, uint64_t ct, uint64_t tile_rows,
                    uint32_t box_rows) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return false;
-  const cuuint64_t dims[2] = {ct * 128, tile_rows};
+  const cuuint64_t dims[2] = {ct * 64, tile_rows};
   const cuuint64_t strides[1] = {ct * 512};
   const cuuint32_t box[2] = {256, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<uint8_t*>(scales), dims, strides, box,
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<uint8_t*>(scales), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -594,7 +619,6 @@ gptq_status by_tokens(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, u
   if (p.M <= 16) return launch_few<16, T>(st, xc, wc, row_bytes, p, sms, status);
   if (p.M <= 32) return launch_few<32, T>(st, xc, wc, row_bytes, p, sms, status);
   if (p.M <= 64) return launch_few<64, T>(st, xc, wc, row_bytes, p, sms, status);
-  if (p.M <= 128) return launch_few<128, T>(st, xc, wc, row_bytes, p, sms, status);
   // the widest token tile by the time of the pairs' waves, in cycles: a step takes about
   // 64 + bn/4 (shared memory moves 4 KB of W and bn/64 KB of X in and out), a tile of a single
   // accumulator starts late
@@ -602,11 +626,12 @@ gptq_status by_tokens(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, u
   p.ntr = (p.R + 255) / 256;
   for (int bn = 256; bn >= 64; bn -= 64) {
     const int64_t tiles = int64_t(p.ntr) * ((p.M + bn - 1) / bn), pairs = sms / 2;
-    const int64_t time = (tiles + pairs - 1) / pairs * (int64_t(p.steps) * (64 + bn / 4) + (bn > 192 ? 2000 : 200));
+    const int64_t time = (tiles + pairs - 1) / pairs * (int64_t(p.steps) * (64 + bn / 4) + (pair::accs_of(bn) == 1 ? 2000 : 200));
     if (best == 0 || time < best) { best = time; p.bn = bn; }
   }
-  p.accs = p.bn > 192 ? 1 : 2;
-  p.nb = (p.bn + 127) / 128;      // 64 and 192 tokens start on either half of a scale tile
+  p.accs = pair::accs_of(p.bn);
+  p.nb = pair::tile_nb(p.bn);
+  p.stages = pair::stages_of(p.bn);
   p.ntt = (p.M + p.bn - 1) / p.bn;
   return launch_pair<T>(st, xc, wc, row_bytes, p, sms, status);
 }
