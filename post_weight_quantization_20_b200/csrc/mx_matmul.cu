@@ -15,7 +15,8 @@
 //              tokens, where the weights' bytes are the work and row tiles alone would leave
 //              SMs idle.
 //  k_mx_pair   256 layer rows x up to 256 tokens per CTA pair (cta_group::2), persistent:
-//              many tokens.
+//              many tokens; where the tiles are few, up to four pairs share a tile's K in the
+//              same way.
 // Every mbarrier wait is bounded; a wait that gives up sets GPTQ_ERR_TIMEOUT and the CTA
 // drains its own copies and MMAs before it frees TMEM and exits.
 #include <algorithm>
@@ -272,6 +273,7 @@ namespace pair {
 // tokens only (256 cycles at 128 tokens).  The ring's shape goes with the token tile.
 constexpr int SUB = 2;                            // boxes of a stage
 constexpr int MAX_STAGES = 5;
+constexpr int MAX_SPLITS = 4;                     // pairs that share a tile's K
 constexpr int RING = 222 * 1024;                  // bytes of shared memory for the stages
 constexpr int SMEM = RING + 1024 /*align*/ + 256 /*barriers*/;
 constexpr int NB = 2;                             // scale tiles that a token tile touches at most
@@ -290,7 +292,8 @@ __host__ __device__ constexpr int stages_of(int bn) {
 }
 __host__ __device__ constexpr int accs_of(int bn) { return bn <= 128 ? 2 : 1; }
 constexpr bool fits(int bn) {
-  return accs_of(bn) * bn + stages_of(bn) * sf_cols(tile_nb(bn)) <= 512 && stages_of(bn) >= 3 &&
+  return bn * 512 <= RING &&
+         accs_of(bn) * bn + stages_of(bn) * sf_cols(tile_nb(bn)) <= 512 && stages_of(bn) >= 3 &&
          stage_bytes(bn, tile_nb(bn)) % 1024 == 0;
 }
 static_assert(fits(64) && fits(128) && fits(192) && fits(256), "TMEM, shared memory");
@@ -306,7 +309,7 @@ __device__ __forceinline__ void tile_of(const Prob& p, int t, int& r0, int& n0) 
 }
 
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS, 1)
 k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
           const __grid_constant__ CUtensorMap wsmap, const __grid_constant__ CUtensorMap xsmap,
           Prob p, uint32_t idesc, int32_t* status) {
@@ -323,10 +326,13 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   uint32_t* issued_slot = tmem_slot + 2;          // the partner's fill count (abort path)
 
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const uint32_t rank = tc::cluster_rank();
-  const int pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  // a cluster is one pair, or the pairs that share a tile's K (one tile per cluster then)
+  const uint32_t base = tc::cluster_rank() & ~1u, rank = tc::cluster_rank() & 1u;
+  const int split = int(base >> 1), splits = int(tc::cluster_size() >> 1);
+  const int pair_id = int(blockIdx.x) / (2 * splits), n_pairs = int(gridDim.x) / (2 * splits);
   const int tiles = p.ntr * p.ntt;
-  const int nk = (p.boxes + SUB - 1) / SUB;       // stages of a tile
+  const int nk = (p.boxes + SUB - 1) / SUB;       // stages along K; this pair's: k0 .. k1 - 1
+  const int k0 = int(int64_t(nk) * split / splits), k1 = int(int64_t(nk) * (split + 1) / splits);
   const int stages = p.stages, bytes = stage_bytes(p.bn, p.nb), cols = sf_cols(p.nb);
   const uint32_t sf_base = 512 - uint32_t(stages * cols);      // TMEM columns below: accumulators
 
@@ -358,7 +364,8 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   tc::cluster_sync();                             // both CTAs' barriers and TMEM ready
   tc::fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t peer_flag = tc::cluster_addr(const_cast<int*>(abort_flag), rank ^ 1u);
+  const uint16_t both = uint16_t(0x3u << base);   // the pair's CTAs in the cluster
+  const uint32_t peer_flag = tc::cluster_addr(const_cast<int*>(abort_flag), base + (rank ^ 1u));
   int64_t issued = 0;
 
   // one fill: boxes past the tensors' ends read as zeros and count in full
@@ -367,7 +374,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     uint8_t* x = a + x_off();
     uint8_t* s = a + s_off(p.bn);
     if (rank == 0) tc::mbar_expect_tx(full + stage, 2 * uint32_t(bytes));
-    const uint32_t cbar = tc::cluster_addr(full + stage, 0);
+    const uint32_t cbar = tc::cluster_addr(full + stage, base);
     const int ra = r0 + 128 * int(rank), rx = n0 + p.bn / 2 * int(rank);
 #pragma unroll
     for (int j = 0; j < SUB; ++j) {
@@ -389,7 +396,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     for (int t = pair_id; t < tiles && ok; t += n_pairs) {
       int r0, n0;
       tile_of(p, t, r0, n0);
-      for (int k = 0; k < nk; ++k) {
+      for (int k = k0; k < k1; ++k) {
         if (!wait(empty + stage, phase ^ 1u)) { ok = false; break; }
         if (tc::elect_one()) load(stage, k, r0, n0);
         __syncwarp();
@@ -423,7 +430,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         if (!wait(acc_empty + acc, acc_phase ^ 1u, true)) break;
         const uint32_t d = tmem_base + uint32_t(acc * p.bn);
         tc::fence_after_sync();
-        for (int k = 0; k < nk; ++k) {
+        for (int k = k0; k < k1; ++k) {
           if (!wait(full + stage, phase)) { ok = false; break; }
           tc::fence_after_sync();
           const uint64_t ad = adesc0 + uint32_t(stage * (bytes >> 4));
@@ -447,9 +454,9 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                 tc::mma_mxf4_pair(d, ad + (kk >> 2) * (A_BOX >> 4) + 2 * (kk & 3),
                                   xd + (kk >> 2) * xbox + 2 * (kk & 3),
                                   idesc | ((kk & 1) ? ODD_HALF : 0u), sfa + 4 * (kk >> 1),
-                                  sfb + first + tile_cols * (kk >> 1), (k > 0 || kk > 0) ? 1u : 0u);
-            tc::mma_commit_pair(empty + stage, 0x3);
-            if (k + 1 == nk) tc::mma_commit_pair(acc_full + acc, 0x3);
+                                  sfb + first + tile_cols * (kk >> 1), (k > k0 || kk > 0) ? 1u : 0u);
+            tc::mma_commit_pair(empty + stage, both);
+            if (k + 1 == k1) tc::mma_commit_pair(acc_full + acc, both);
           }
           __syncwarp();
           if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -460,7 +467,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   } else {
     const int lane_base = (warp & 3) * 32;
     const int half = p.bn / 2, c0 = ((warp - 2) >> 2) * half;     // this warp's tokens of the tile
-    const uint32_t acc_empty0 = tc::cluster_addr(acc_empty, 0);
+    const uint32_t acc_empty0 = tc::cluster_addr(acc_empty, base);
     uint32_t acc_phase = 0;
     int acc = 0;
     for (int t = pair_id; t < tiles; t += n_pairs) {
@@ -479,7 +486,16 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
       if (lane == 0) tc::mbar_arrive_cluster_relaxed(acc_empty0 + uint32_t(acc * 8));
       if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
       const int row = r0 + 128 * int(rank) + lane_base + lane;
-      if (row < p.R) {
+      if (splits > 1) {
+        // this pair's partial sums, [token][128 rows]; every load into the ring was consumed
+        float* part = reinterpret_cast<float*>(smem) + c0 * 128 + lane_base + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (32 * c < half) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) part[(32 * c + i) * 128] = __uint_as_float(v[c][i]);
+          }
+      } else if (row < p.R) {
         const int live = min(half, p.M - n0 - c0);
         T* y = static_cast<T*>(p.Y) + int64_t(n0 + c0) * p.ldy + row;
 #pragma unroll
@@ -503,7 +519,46 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   }
   tc::fence_before_sync();
   __syncthreads();
-  tc::cluster_sync_relaxed();  // both CTAs out of their loops: the abort flags are final
+  if (splits > 1) {
+    // an abort is the whole cluster's: the barriers below are
+    if (threadIdx.x == 0 && *abort_flag) {
+      for (int q = 0; q < 2 * splits; ++q)
+        tc::st_cluster_u32(tc::cluster_addr(const_cast<int*>(abort_flag), uint32_t(q)), 1u);
+      asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    tc::cluster_sync();        // the partial sums are written
+    if (!*abort_flag) {
+      // every pair sums its share of the tokens, the splits in order (a warp a token, a lane
+      // four layer rows, all loads before the first sum)
+      int r0, n0;
+      tile_of(p, pair_id, r0, n0);
+      const int live = min(p.bn, p.M - n0), row = r0 + 128 * int(rank) + 4 * lane;
+      for (int t = split + splits * warp; t < live; t += splits * (THREADS / 32)) {
+        const uint32_t at = tc::smem_u32(smem + (t * 128 + 4 * lane) * 4);
+        float4 part[MAX_SPLITS];
+#pragma unroll
+        for (int q = 0; q < MAX_SPLITS; ++q)
+          if (q < splits) part[q] = tc::ld_cluster_f32x4(tc::map_cluster(at, uint32_t(2 * q) + rank));
+        float4 v = part[0];
+#pragma unroll
+        for (int q = 1; q < MAX_SPLITS; ++q)
+          if (q < splits) {
+            v.x += part[q].x;
+            v.y += part[q].y;
+            v.z += part[q].z;
+            v.w += part[q].w;
+          }
+        T* y = static_cast<T*>(p.Y) + int64_t(n0 + t) * p.ldy + row;
+        const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row + i < p.R) y[i] = from_f32<T>(o[i]);
+      }
+    }
+    __syncwarp();
+  }
+  tc::cluster_sync_relaxed();  // all CTAs out of their loops: the abort flags are final
   if (*abort_flag) {
     // A wait gave up in one of the CTAs, which raised both flags.  (1) rank 0's MMAs land;
     // (2) the producers exchange their fill counts and the one behind fills the phases the
@@ -512,13 +567,13 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     // (4) neither CTA exits before that.
     if (warp == 1 && rank == 0) {    // by the lane that issued the MMAs
       if (tc::elect_one()) {
-        tc::mma_commit_pair(drain, 0x1);
+        tc::mma_commit_pair(drain, uint16_t(1u << base));
         tc::mbar_drain(drain, 0);
       }
       __syncwarp();
     }
     if (warp == 0 && lane == 0)
-      tc::st_cluster_u32(tc::cluster_addr(issued_slot, rank ^ 1u), uint32_t(issued));
+      tc::st_cluster_u32(tc::cluster_addr(issued_slot, base + (rank ^ 1u)), uint32_t(issued));
     tc::fence_before_sync();
     tc::cluster_sync();
     if (warp == 0 && lane == 0) {
@@ -568,6 +623,27 @@ bool encode_scales(CUtensorMap* m, const uint8_t* scales, uint64_t ct, uint64_t 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of CTAs that fill an SM each that run at once: SMs come in groups whose size is no
+// multiple of 4 or 8 (148 SMs: 74 clusters of 2, 33 of 4, 15 of 8 by the occupancy query).
+int64_t clusters_at_once(int ctas, int sms) {
+  return ctas <= 2 ? sms / ctas : ctas <= 4 ? sms * 2 / 9 : sms / 10;
+}
+
+cudaLaunchConfig_t cluster_launch(unsigned x, unsigned y, int cluster, int threads, int smem,
+                                  cudaStream_t st, cudaLaunchAttribute& at) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(x, y);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = unsigned(cluster);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
 template <int BN, typename T>
 gptq_status launch_few(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, uint64_t row_bytes,
                        const Prob& p, int sms, int32_t* status) {
@@ -578,20 +654,13 @@ gptq_status launch_few(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, 
     return GPTQ_ERR_UNSUPPORTED;
   const int rows = (p.R + 127) / 128, cols = (p.M + BN - 1) / BN;
   int splits = 1;
-  while (splits < 8 && int64_t(rows) * cols * splits * 2 <= sms && p.boxes >= 2 * C::SUB * splits)
+  while (splits < 8 && int64_t(rows) * cols <= clusters_at_once(2 * splits, sms) &&
+         p.boxes >= 2 * C::SUB * splits)
     splits *= 2;
   GPTQ_CUDA(allow_smem(k_mx_few<BN, T>, C::SMEM));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(rows * splits), unsigned(cols));
-  cfg.blockDim = dim3(FEW_THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(splits);
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = cluster_launch(unsigned(rows * splits), unsigned(cols), splits,
+                                                FEW_THREADS, C::SMEM, st, at);
   GPTQ_CUDA(cudaLaunchKernelEx(&cfg, k_mx_few<BN, T>, wmap, xmap, p, status));
   note_launch();
   return GPTQ_OK;
@@ -599,7 +668,7 @@ gptq_status launch_few(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, 
 
 template <typename T>
 gptq_status launch_pair(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, uint64_t row_bytes,
-                        Prob p, int sms, int32_t* status) {
+                        const Prob& p, int splits, int sms, int32_t* status) {
   CUtensorMap wmap, xmap, wsmap, xsmap;
   if (!encode_codes(&wmap, wc, row_bytes, uint64_t(p.R), 128) ||
       !encode_codes(&xmap, xc, row_bytes, uint64_t(p.M), uint32_t(p.bn / 2)) ||
@@ -607,33 +676,48 @@ gptq_status launch_pair(cudaStream_t st, const uint32_t* xc, const uint32_t* wc,
       !encode_scales(&xsmap, p.xs, uint64_t(p.ct), uint64_t((p.M + 127) / 128), uint32_t(p.nb)))
     return GPTQ_ERR_UNSUPPORTED;
   GPTQ_CUDA(allow_smem(pair::k_mx_pair<T>, pair::SMEM));
-  const int pairs = int(std::min<int64_t>(sms / 2, int64_t(p.ntr) * p.ntt));
-  GPTQ_LAUNCH(pair::k_mx_pair<T>, 2 * pairs, pair::THREADS, pair::SMEM, st, wmap, xmap, wsmap, xsmap,
-              p, idesc_of(256, p.bn), status);
+  const int clusters = int(std::min<int64_t>(sms / (2 * splits), int64_t(p.ntr) * p.ntt));
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = cluster_launch(unsigned(2 * splits * clusters), 1, 2 * splits,
+                                                pair::THREADS, pair::SMEM, st, at);
+  GPTQ_CUDA(cudaLaunchKernelEx(&cfg, pair::k_mx_pair<T>, wmap, xmap, wsmap, xsmap, p,
+                               idesc_of(256, p.bn), status));
+  note_launch();
   return GPTQ_OK;
 }
 
 template <typename T>
 gptq_status by_tokens(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, uint64_t row_bytes,
                       Prob p, int sms, int32_t* status) {
+  // K split over clusters where there are few tokens or few layer rows.  Measured (few tokens'
+  // kernel against pairs, us): 16 tokens 4096 x 11008 6.4 / 11.9, 49152 x 12288 55.7 / 53.9; 64
+  // tokens 4096 x 11008 7.9 / 12.2, 5120 x 5120 7.7 / 7.8, 11008 x 4096 8.3 / 7.2, 49152 x 12288
+  // 64.9 / 54.0; 128 tokens 12288 x 12288 21.7 / 14.2.
+  p.ntr = (p.R + 255) / 256;
   if (p.M <= 16) return launch_few<16, T>(st, xc, wc, row_bytes, p, sms, status);
   if (p.M <= 32) return launch_few<32, T>(st, xc, wc, row_bytes, p, sms, status);
-  if (p.M <= 64) return launch_few<64, T>(st, xc, wc, row_bytes, p, sms, status);
-  // the widest token tile by the time of the pairs' waves, in cycles: a step takes about
-  // 64 + bn/4 (shared memory moves 4 KB of W and bn/64 KB of X in and out), a tile of a single
-  // accumulator starts late
+  if (p.M <= 64 && 4 * p.ntr <= sms) return launch_few<64, T>(st, xc, wc, row_bytes, p, sms, status);
+  // the token tile, and the pairs that share its K, by the time of the pairs' waves in cycles: a
+  // step takes about 64 + bn/4 (operand bytes into shared memory: 4 KB of W, bn/64 KB of X), a
+  // tile of a single accumulator starts late, partial sums are written and read again
   int64_t best = 0;
-  p.ntr = (p.R + 255) / 256;
+  int splits = 1;
+  const int64_t pairs = sms / 2;
+  const int nk = (p.boxes + pair::SUB - 1) / pair::SUB;
   for (int bn = 256; bn >= 64; bn -= 64) {
-    const int64_t tiles = int64_t(p.ntr) * ((p.M + bn - 1) / bn), pairs = sms / 2;
-    const int64_t time = (tiles + pairs - 1) / pairs * (int64_t(p.steps) * (64 + bn / 4) + (pair::accs_of(bn) == 1 ? 2000 : 200));
-    if (best == 0 || time < best) { best = time; p.bn = bn; }
+    const int64_t tiles = int64_t(p.ntr) * ((p.M + bn - 1) / bn);
+    for (int s = 1; s <= pair::MAX_SPLITS && (s == 1 || (tiles <= clusters_at_once(2 * s, sms) && nk >= 2 * s)); s *= 2) {
+      const int64_t steps = s == 1 ? p.steps : int64_t((nk + s - 1) / s) * 4 * pair::SUB;
+      const int64_t time = (tiles * s + pairs - 1) / pairs * (steps * (64 + bn / 4) + (pair::accs_of(bn) == 1 ? 2000 : 200)) +
+                           (s > 1 ? 1500 + 8 * bn : 0);
+      if (best == 0 || time < best) { best = time; p.bn = bn; splits = s; }
+    }
   }
   p.accs = pair::accs_of(p.bn);
   p.nb = pair::tile_nb(p.bn);
   p.stages = pair::stages_of(p.bn);
   p.ntt = (p.M + p.bn - 1) / p.bn;
-  return launch_pair<T>(st, xc, wc, row_bytes, p, sms, status);
+  return launch_pair<T>(st, xc, wc, row_bytes, p, splits, sms, status);
 }
 
 }  // namespace

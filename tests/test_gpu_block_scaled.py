@@ -154,7 +154,9 @@ SHAPES = [(1, 128, 64), (1, 1, 1), (2, 130, 32), (1, 513, 4128), (3, 100, 96), (
           (129, 300, 640), (256, 256, 1024), (300, 200, 4104), (257, 1000, 160), (700, 515, 1056),
           (1, 4096, 12288), (5, 640, 20000), (520, 130, 8200),
           # every width of a token tile, tiles that start in the middle of 128 tokens among them
-          (256, 5120, 96), (384, 9472, 96), (500, 9472, 64), (700, 9472, 33)]
+          (256, 5120, 96), (384, 9472, 96), (500, 9472, 64), (700, 9472, 33),
+          # few tiles and a long K, which several pairs share
+          (100, 300, 20000), (333, 513, 8200), (700, 130, 33000), (65, 2000, 1056), (129, 4000, 2100)]
 
 
 @pytest.mark.parametrize("M,R,C", SHAPES)
@@ -179,7 +181,8 @@ def test_product_within_its_bound(M, R, C, dtype):
     assert out.intact() and (out.t[:, R:] == 7.0).all()
 
 
-@pytest.mark.parametrize("M,R,C", [(1, 200, 4128), (40, 300, 2080), (130, 257, 1056), (513, 514, 5152)])
+@pytest.mark.parametrize("M,R,C", [(1, 200, 4128), (40, 300, 2080), (130, 257, 1056), (513, 514, 5152),
+                                   (100, 300, 9000), (300, 1030, 4160)])
 def test_product_of_small_whole_numbers_is_exact(M, R, C):
     # every scale 1: products are multiples of 1/4 and every sum stays below 2^24 of them
     xc, xs, x = _stored(M, C, 1, 127, 128)
