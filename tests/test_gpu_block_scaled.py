@@ -292,3 +292,30 @@ def test_product_output_past_32_bit_offsets():
     Y = MX.mx_matmul(x, w, torch.bfloat16)
     assert float(Y[0, 0]) == 1 and float(Y[M - 1, R - 1]) == 6 and float(Y[M - 1, 0]) == 2
     assert float(Y[M - 2, R - 1]) == 3 and float(Y[M // 2].float().sum()) == R + 2
+
+
+@pytest.mark.parametrize("M,R,C,shared", [(4, 1500, 49152, False), (512, 1500, 49152, False),
+                                          (16, 300, 49152, True), (300, 1000, 49152, True)])
+def test_product_waits_give_up_and_drain(M, R, C, shared):
+    # with a limit of one poll the waits run out during normal work: the status says so, the
+    # context stays usable and the same call then computes the right values.  Where CTAs share
+    # a tile's K (`shared`) a poll may outlast the work; then the values are right at once
+    xc, xs, x = _stored(M, C, 1, 127, 128)
+    wc, ws, w = _stored(R, C, 2, 127, 128)
+    Y = torch.empty(M, R, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    old = G.gptq_debug_set_wait_limit(1)
+    try:
+        for _ in range(3):
+            MX.gptq_mx_matmul(xc, xs, wc, ws, C, Y, st)
+        torch.cuda.synchronize()
+    finally:
+        G.gptq_debug_set_wait_limit(0)
+    assert old > 1 and int(st) in ((0, G.GPTQ_ERR_TIMEOUT) if shared else (G.GPTQ_ERR_TIMEOUT,))
+    if int(st):
+        st.zero_()
+        MX.gptq_mx_matmul(xc, xs, wc, ws, C, Y, st)
+    # multiples of 1/4 whose sums stay below 2^24 of them
+    rows = slice(0, 300)
+    np.testing.assert_array_equal(Y[:, rows].double().cpu().numpy(), x @ w[rows].T)
+    assert int(st) == 0
