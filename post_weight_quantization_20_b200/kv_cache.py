@@ -20,7 +20,7 @@ from dataclasses import dataclass
 import torch
 
 from . import gptq as G
-from .mx import _WORDS, _call, _expect, _need_one_device, _status_ptr, mx_words
+from .mx import _WORDS, _call, _status_ptr, mx_words
 
 GPTQ_CACHE_GRID, GPTQ_CACHE_MX = 0, 1
 
@@ -113,9 +113,8 @@ def _no_overlap(t, name):
         raise ValueError(f"the rows of {name} must not overlap")
 
 
-def _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, status,
-             written=False):
-    """Check a call's tensors; the arguments of the C call that both directions share."""
+def _explain(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, written):
+    """Raise for the first tensor of a call that does not fit."""
     _expect_rows_of(K, "K")
     _expect_rows_of(V, "V")
     if V.shape != K.shape or V.dtype != K.dtype:
@@ -123,51 +122,82 @@ def _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, st
     if written:
         _no_overlap(K, "K")
         _no_overlap(V, "V")
-    T, H, D = K.shape
     if k_codes.dim() != 4:
         raise ValueError("k_codes must be 4-D (pages, page_size, heads, words)")
-    pages, page_size, _, _ = k_codes.shape
+    pages, page_size = k_codes.shape[:2]
+    _, H, D = K.shape
     shape = (pages, page_size, H, _words(cfg, D))
-    _expect(k_codes, "k_codes", shape, _WORDS)
-    _expect(v_codes, "v_codes", shape, _WORDS)
+    G._expect(k_codes, "k_codes", shape, _WORDS)
+    G._expect(v_codes, "v_codes", shape, _WORDS)
     shape, dtype = _grid_shape(cfg, pages, page_size, H, D)
-    _expect(k_grids, "k_grids", shape, (dtype,))
-    _expect(v_grids, "v_grids", shape, (dtype,))
+    G._expect(k_grids, "k_grids", shape, (dtype,))
+    G._expect(v_grids, "v_grids", shape, (dtype,))
     if table.dim() != 2 or table.dtype != torch.int32 or (table.shape[1] > 1 and table.stride(1) != 1):
         raise ValueError("table must be an int32 (seqs, width) tensor with unit column stride")
     S, width = table.shape
-    ld = table.stride(0) if S > 1 else width
-    if ld < width:
+    if S > 1 and table.stride(0) < width:
         raise ValueError("the rows of table must not overlap")
-    _expect(cu, "cu", (S + 1,), (torch.int32,))
-    _expect(start, "start", (S,), (torch.int32,))
+    G._expect(cu, "cu", (S + 1,), (torch.int32,))
+    G._expect(start, "start", (S,), (torch.int32,))
+
+
+_I32 = torch.int32
+
+
+def _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, status,
+             written=False):
+    """Check a call's tensors; the arguments of the C call that both directions share.  One
+    expression passes what fits; _explain says what does not."""
+    fits = False
+    if K.dim() == 3 and k_codes.dim() == 4 and table.dim() == 2 and V.shape == K.shape:
+        T, H, D = K.shape
+        (kt, kh, k1), (vt, vh, v1) = K.stride(), V.stride()
+        pages, page_size, _, _ = k_codes.shape
+        (S, width), (ld, one) = table.shape, table.stride()
+        codes = (pages, page_size, H, _words(cfg, D))
+        grids, gtype = _grid_shape(cfg, pages, page_size, H, D)
+        if S <= 1:
+            ld = width
+        fits = (k_codes.shape == codes and v_codes.shape == codes and k_grids.shape == grids
+                and v_grids.shape == grids and k_codes.dtype in _WORDS and v_codes.dtype in _WORDS
+                and k_grids.dtype is gtype and v_grids.dtype is gtype and k_codes.is_contiguous()
+                and v_codes.is_contiguous() and k_grids.is_contiguous() and v_grids.is_contiguous()
+                and (k1 == v1 == 1 or D == 1) and V.dtype is K.dtype and K.dtype in G._DT
+                and table.dtype is _I32 and (one == 1 or width <= 1) and ld >= width
+                and cu.shape == (S + 1,) and start.shape == (S,) and cu.dtype is _I32
+                and start.dtype is _I32 and cu.is_contiguous() and start.is_contiguous()
+                and not (written and not (K.is_contiguous() and V.is_contiguous())))
+    if not fits:
+        _explain(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, written)
     st = _status_ptr(status)
-    _need_one_device(K, V, k_codes, k_grids, v_codes, v_grids, table, cu, start, status)
+    dev = K.get_device()
+    if dev < 0 or st is not None or not (
+            dev == V.get_device() == k_codes.get_device() == k_grids.get_device()
+            == v_codes.get_device() == v_grids.get_device() == table.get_device()
+            == cu.get_device() == start.get_device()):
+        G._need_cuda(K, V, k_codes, k_grids, v_codes, v_grids, table, cu, start, status)
     cache = gptq_cache(k_codes.data_ptr(), k_grids.data_ptr(), v_codes.data_ptr(),
                        v_grids.data_ptr(), pages, page_size, H, D)
     rows = gptq_cache_rows(table.data_ptr(), ld, width, cu.data_ptr(), start.data_ptr(), S)
     where = (ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rows))
-    (kt, kh, _), (vt, vh, _) = K.stride(), V.stride()
     data = (K.data_ptr(), V.data_ptr(), G._DT[K.dtype], T, kt, kh, vt, vh)
-    return where, data, st
+    return dev, where, data, st
 
 
 def gptq_cache_write(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, status=None,
                      stream=None) -> None:
     """Quantise the rows of K and V (rows, heads, dim) into their slots of the cache."""
-    where, data, st = _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start,
-                               status)
-    load_library()
-    _call("gptq_cache_write", K, stream, *data, *where, st)
+    dev, where, data, st = _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu,
+                                    start, status)
+    _call(load_library().gptq_cache_write, "gptq_cache_write", dev, stream, *data, *where, st)
 
 
 def gptq_cache_read(cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, K, V, status=None,
                     stream=None) -> None:
     """The rows' values out of their slots of the cache into K and V (rows, heads, dim)."""
-    where, data, st = _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start,
-                               status, written=True)
-    load_library()
-    _call("gptq_cache_read", K, stream, *where, *data, st)
+    dev, where, data, st = _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu,
+                                    start, status, written=True)
+    _call(load_library().gptq_cache_read, "gptq_cache_read", dev, stream, *where, *data, st)
 
 
 # --------------------------------------------------------------------------- one cache

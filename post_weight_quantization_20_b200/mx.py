@@ -59,39 +59,25 @@ def gptq_mx_scale_bytes(rows: int, cols: int) -> int:
 _WORDS = (torch.int32, torch.uint32)
 
 
-def _call(name, where, stream, *args):
-    """Call the library on `stream` of the device of the tensor `where`, which is made the
-    current one (a launch and its stream belong to it)."""
-    dev = where.get_device()
-    f = getattr(load_library(), name)
+def _call(f, name, dev, stream, *args):
+    """Call the library's `f` on `stream` (default: the current one) of device `dev`, which is
+    made the current one: a launch and its stream belong to it."""
     if dev == torch._C._cuda_getDevice():
-        code = f(*args, _raw_stream(stream, dev))
+        code = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            code = f(*args, _raw_stream(stream, dev))
+            code = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if code:
         G._check(code, name)
 
 
-def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _need_one_device(first, *others):
-    """Device tensors, all on one device (None is left out)."""
-    dev = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            break
-    else:
-        if dev >= 0:
-            return
-    G._need_cuda(first, *others)
-
-
-def _expect(t, name, shape, dtypes):
-    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
-        G._expect(t, name, shape, dtypes)
+def _expect_stored(codes, scales, rows, cols, name=""):
+    """Raise unless codes and scales are the stored form of a rows x cols matrix."""
+    words, shape = (rows, (cols + 31) // 32 * 4), mx_scale_shape(rows, cols)
+    if not (codes.shape == words and scales.shape == shape and codes.dtype in _WORDS
+            and scales.dtype is torch.uint8 and codes.is_contiguous() and scales.is_contiguous()):
+        G._expect(codes, name + "codes", words, _WORDS)
+        G._expect(scales, name + "scales", shape, (torch.uint8,))
 
 
 def _expect_matrix(t, name):
@@ -111,11 +97,6 @@ def _expect_matrix(t, name):
     return R, C, dt, ld
 
 
-def _expect_stored(codes, scales, rows, cols, name=""):
-    _expect(codes, name + "codes", (rows, mx_words(cols)), _WORDS)
-    _expect(scales, name + "scales", mx_scale_shape(rows, cols), (torch.uint8,))
-
-
 def _status_ptr(status):
     if status is None:
         return None
@@ -128,18 +109,22 @@ def gptq_mx_quantize(X, codes, scales, status=None, stream=None) -> None:
     R, C, dt, ld = _expect_matrix(X, "X")
     _expect_stored(codes, scales, R, C)
     st = _status_ptr(status)
-    _need_one_device(X, codes, scales, status)
-    _call("gptq_mx_quantize", X, stream, X.data_ptr(), dt, R, C, ld, codes.data_ptr(),
-          scales.data_ptr(), st)
+    dev = X.get_device()
+    if dev < 0 or codes.get_device() != dev or scales.get_device() != dev or st is not None:
+        G._need_cuda(X, codes, scales, status)
+    _call(load_library().gptq_mx_quantize, "gptq_mx_quantize", dev, stream, X.data_ptr(), dt, R, C,
+          ld, codes.data_ptr(), scales.data_ptr(), st)
 
 
 def gptq_mx_dequantize(codes, scales, Y, stream=None) -> None:
     """Y (rows x cols) = the values the stored form stands for."""
     R, C, dt, ld = _expect_matrix(Y, "Y")
     _expect_stored(codes, scales, R, C)
-    _need_one_device(Y, codes, scales)
-    _call("gptq_mx_dequantize", Y, stream, codes.data_ptr(), scales.data_ptr(), R, C,
-          Y.data_ptr(), dt, ld)
+    dev = Y.get_device()
+    if dev < 0 or codes.get_device() != dev or scales.get_device() != dev:
+        G._need_cuda(codes, scales, Y)
+    _call(load_library().gptq_mx_dequantize, "gptq_mx_dequantize", dev, stream, codes.data_ptr(),
+          scales.data_ptr(), R, C, Y.data_ptr(), dt, ld)
 
 
 def gptq_mx_matmul(x_codes, x_scales, w_codes, w_scales, cols, Y, status=None,
@@ -150,9 +135,13 @@ def gptq_mx_matmul(x_codes, x_scales, w_codes, w_scales, cols, Y, status=None,
     _expect_stored(x_codes, x_scales, M, cols, "x_")
     _expect_stored(w_codes, w_scales, R, cols, "w_")
     st = _status_ptr(status)
-    _need_one_device(Y, x_codes, x_scales, w_codes, w_scales, status)
-    _call("gptq_mx_matmul", Y, stream, x_codes.data_ptr(), x_scales.data_ptr(), M,
-          w_codes.data_ptr(), w_scales.data_ptr(), R, cols, Y.data_ptr(), dt, ld, st)
+    dev = Y.get_device()
+    if dev < 0 or st is not None or not (dev == x_codes.get_device() == x_scales.get_device()
+                                         == w_codes.get_device() == w_scales.get_device()):
+        G._need_cuda(x_codes, x_scales, w_codes, w_scales, Y, status)
+    _call(load_library().gptq_mx_matmul, "gptq_mx_matmul", dev, stream, x_codes.data_ptr(),
+          x_scales.data_ptr(), M, w_codes.data_ptr(), w_scales.data_ptr(), R, cols, Y.data_ptr(),
+          dt, ld, st)
 
 
 # --------------------------------------------------------------------------- whole matrices
