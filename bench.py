@@ -3,6 +3,7 @@
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
                     [--workload opt175b]
     python bench.py --op hessian|prepare|quantize|layer --rows R --cols C --tokens T
+    python bench.py --op mx_quantize|mx_matmul|cache_write|cache_read --rows R --cols C --tokens T
 
 One step quantizes every layer of the workload once: Hessian accumulation over
 all calibration tokens, damping / ordering / inverse Cholesky factor, the
@@ -687,6 +688,61 @@ def run_reference(args):
 
 
 # ----------------------------------------------------------------------------- one stage
+LOWBIT_OPS = ("mx_quantize", "mx_dequantize", "mx_matmul", "cache_write", "cache_read")
+
+
+def run_lowbit_op(args):
+    """Time one of the 4-bit operators on device-drawn inputs; one text line.  The matrices
+    are rows x cols, the products take `tokens` tokens; the cache calls take `tokens` rows of
+    8 heads x 128 in 64-token pages, 4 or 8 bits on grids of `group` values (0: a head)."""
+    import torch
+    from post_weight_quantization_20_b200 import gptq as G
+    from post_weight_quantization_20_b200 import kv_cache as KV
+    from post_weight_quantization_20_b200 import mx as MX
+    dev = torch.device("cuda", torch.cuda.current_device())
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(0)
+    R, C, T = args.rows, args.cols, args.tokens
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    if args.op.startswith("mx_"):
+        W = (0.02 * torch.randn(R, C, device=dev, generator=gen)).bfloat16()
+        w = MX.mx_quantize(W, status)
+        if args.op == "mx_matmul":
+            x = MX.mx_quantize(torch.randn(T, C, device=dev, generator=gen).bfloat16(), status)
+            Y = torch.empty(T, R, dtype=torch.bfloat16, device=dev)
+
+            def run():
+                MX.gptq_mx_matmul(x.codes, x.scales, w.codes, w.scales, C, Y, status)
+            work = f"{2.0 * T * R * C / 1e12:.4f} TFLOP, {(w.nbytes + x.nbytes + 2 * T * R) / 1e6:.1f} MB per call"
+        else:
+            def run():
+                if args.op == "mx_quantize":
+                    MX.gptq_mx_quantize(W, w.codes, w.scales, status)
+                else:
+                    MX.gptq_mx_dequantize(w.codes, w.scales, W)
+            work = f"{(w.nbytes + 2 * R * C) / 1e6:.1f} MB per call"
+    else:
+        heads, dim, page = 8, 128, 64
+        cfg = KV.make_cache_config("grid", args.bits, args.group)
+        pages = (T + page - 1) // page
+        cache = KV.KVCache.alloc(cfg, pages, page, heads, dim, dev)
+        K = torch.randn(T, heads, dim, device=dev, generator=gen).bfloat16()
+        V = torch.randn(T, heads, dim, device=dev, generator=gen).bfloat16()
+        i32 = dict(dtype=torch.int32, device=dev)
+        rows = (torch.randperm(pages, device=dev, generator=gen).to(torch.int32)[None],
+                torch.tensor([0, T], **i32), torch.zeros(1, **i32))
+        cache.write(K, V, *rows, status)
+
+        def run():
+            if args.op == "cache_write":
+                cache.write(K, V, *rows, status)
+            else:
+                KV.gptq_cache_read(cfg, cache.k_codes, cache.k_grids, cache.v_codes, cache.v_grids,
+                                   *rows, K, V, status)
+        work = f"{(cache.nbytes + 4 * T * heads * dim) / 1e6:.1f} MB per call"
+    time_op(args, run, work, status, dev)
+
+
 def run_op(args):
     """Time one stage of one layer on device-drawn inputs; one text line."""
     import torch
@@ -747,6 +803,13 @@ def run_op(args):
         def run():
             G.quantize_layer(W, X, cfg, check=False)
         work = "Hessian + prepare + sweep + pack, with their allocations"
+    time_op(args, run, work, status, dev)
+
+
+def time_op(args, run, work, status, dev):
+    """args.repeat warm-up and as many timed calls of run; prints the time of one."""
+    import torch
+    from post_weight_quantization_20_b200 import gptq as G
     for _ in range(args.repeat):
         run()
     torch.cuda.synchronize(dev)
@@ -760,7 +823,8 @@ def run_op(args):
     torch.cuda.synchronize(dev)
     G.check_status(status, args.op)
     ms = e0.elapsed_time(e1) / args.repeat
-    print(f"op={args.op} rows={R} cols={C} tokens={T}: {ms:.3f} ms per call ({work})", flush=True)
+    print(f"op={args.op} rows={args.rows} cols={args.cols} tokens={args.tokens}: {ms:.3f} ms per call "
+          f"({work})", flush=True)
 
 
 def main():
@@ -772,7 +836,7 @@ def main():
     ap.add_argument("--workload", default="opt175b", choices=sorted(WORKLOADS))
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--op", default="step", choices=["step", "hessian", "prepare", "quantize",
-                                                     "layer", "dequant"])
+                                                     "layer", "dequant", *LOWBIT_OPS])
     ap.add_argument("--rows", type=int, default=768)
     ap.add_argument("--cols", type=int, default=3072)
     ap.add_argument("--tokens", type=int, default=16384)
@@ -782,7 +846,7 @@ def main():
     ap.add_argument("--act-order", action="store_true")
     args = ap.parse_args()
     if args.op != "step":
-        run_op(args)
+        (run_lowbit_op if args.op in LOWBIT_OPS else run_op)(args)
         return
     rank = int(os.environ.get("RANK", "0"))
     world = int(os.environ.get("WORLD_SIZE", "1"))
