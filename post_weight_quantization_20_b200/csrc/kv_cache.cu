@@ -3,8 +3,8 @@
 //
 // Both directions are one pass over the rows, bound by HBM (2 or 4 bytes per value on one
 // side, 4.25 to 10 bits on the other) or, for a token per sequence, by the launch and the
-// chain cu -> start -> table -> slot.  A lane takes 32 bytes of a row to quantise, and a group
-// is 1 to 32 neighbouring lanes, so that its range is a few shuffles and nothing is staged; to
+// chain cu -> start -> table -> slot.  A lane takes 32 or 64 bytes of a row to quantise, and a
+// group is 1 to 16 neighbouring lanes, so that its range is a few shuffles and nothing is staged; to
 // read, a lane writes 16 bytes.  A thread's place in a row (K or V, head, group) is the same in
 // every row that it takes, so it is worked out once.  One thread per row finds its sequence and
 // slot, in a write while the first loads are in flight.
@@ -70,54 +70,69 @@ __device__ __forceinline__ Where find_row(const Args& a, int64_t t, int32_t* sta
 
 enum { GRID4 = 0, GRID8 = 1, MX4 = 2 };
 
-// x / s rounded to fp32 where nothing under- or overflows, without a division: with inv = 1 / s
-// rounded, x * inv is within 1.5 ulp of the quotient, a residual correction brings it within
-// one, and from there a second one gives the correctly rounded quotient (Markstein, IBM J. Res.
-// Dev. 34(1), 1990).  The codes need that rounding: 16-bit values hit exact ties of their grid
-// all the time (15 x / (hi - lo) is a fraction of small whole numbers).  The division itself
-// per value took twice as long (470 us against 240 for 131072 tokens of 8 x 128 bf16 K and V).
-__device__ __forceinline__ float quotient(float x, float s, float inv) {
-  float q = x * inv;
-  q = fmaf(fmaf(-q, s, x), inv, q);
+// x / s rounded to fp32 where nothing under- or overflows, without a division: inv + low is
+// 1 / s to about 48 bits, so that the first q is within half an ulp and a little of the quotient,
+// and from there one residual correction with inv, 1 / s rounded, gives the correctly rounded
+// quotient (Markstein, IBM J. Res. Dev. 34(1), 1990: q within one ulp is enough).  The codes need
+// that rounding: 16-bit values hit exact ties of their grid all the time (15 x / (hi - lo) is a
+// fraction of small whole numbers).  With a division per value a write took 470 us (131072
+// tokens of 8 x 128 bf16 K and V).
+__device__ __forceinline__ float quotient(float x, float s, float inv, float low) {
+  const float q = fmaf(x, inv, x * low);
   return fmaf(fmaf(-q, s, x), inv, q);
 }
+__device__ __forceinline__ float low_part(float s, float inv) { return fmaf(-inv, s, 1.f) * inv; }
 
-// The grid of [lo, hi] and the codes clamp(rint(x / s) + z, 0, maxq) of N values on it, as
-// grid_params defines it; false if the range is not finite.
-template <int N, int maxq>
-__device__ __forceinline__ bool grid_codes(const float (&x)[N], float lo, float hi, int sym, float& s,
-                                           float& z, int (&c)[N]) {
-  const float m = fmaxf(-lo, hi);
-  const float width = sym ? m + m : hi - lo;
-  // no under- or overflow below (not taken by NaN either)
-  if (width > 0x1p-90f && width < 0x1p90f) {
-    s = quotient(width, float(maxq), 1.f / float(maxq));
-    const float inv = __frcp_rn(s);
-    // adding 1.5 * 2^23 rounds to a whole number, which is the sum's low bits
-    constexpr float magic = 12582912.f;
-    constexpr int magic_bits = 0x4B400000;
-    const int zi = sym ? (maxq + 1) / 2
-                       : __float_as_int(quotient(-lo, s, inv) + magic) - magic_bits;
-    z = sym ? float(zi) : copysignf(float(zi), -lo);      // a zero with the sign that rint(-lo / s) has
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      c[i] = __vimin_s32_relu(__float_as_int(quotient(x[i], s, inv) + magic) + (zi - magic_bits), maxq);
-    return true;
+enum { GRID_FAST = 0, GRID_SLOW = 1, GRID_NAN = 2 };
+
+// The grid of [lo, hi] as grid_params defines it, and the codes clamp(rint(x / s) + z, 0, maxq) of
+// values on it.
+template <int maxq>
+struct Grid {
+  float s, z, inv, low;
+  int zi, kind;
+  __device__ __forceinline__ Grid(float lo, float hi, int sym) {
+    const float m = fmaxf(-lo, hi);
+    const float width = sym ? m + m : hi - lo;
+    kind = GRID_FAST;
+    inv = low = 0.f;
+    zi = 0;
+    if (width > 0x1p-90f && width < 0x1p90f) {   // no under- or overflow below (NaN is neither)
+      constexpr float r = 1.f / float(maxq);     // rounded, and what that leaves of 1 / maxq
+      constexpr float rl = float(1.0 / maxq - double(r));
+      s = quotient(width, float(maxq), r, rl);
+      inv = __frcp_rn(s);
+      low = low_part(s, inv);
+      zi = sym ? (maxq + 1) / 2 : whole(quotient(-lo, s, inv, low));
+      z = sym ? float(zi) : copysignf(float(zi), -lo);   // a zero with the sign of rint(-lo / s)
+      return;
+    }
+    kind = GRID_SLOW;
+    grid_params(lo, hi, float(maxq), sym, s, z);
+    if (s == 0.f) grid_params(-1.f, 1.f, float(maxq), sym, s, z);     // an underflowed range
+    if (lo != lo || !(s <= 3.402823466e38f)) {
+      kind = GRID_NAN;
+      s = __uint_as_float(0x7FC00000u);
+      z = 0.f;
+    }
   }
-  grid_params(lo, hi, float(maxq), sym, s, z);
-  if (s == 0.f) grid_params(-1.f, 1.f, float(maxq), sym, s, z);     // an underflowed range
+  // rint(q) of |q| < 2^22: adding 1.5 * 2^23 rounds to a whole number, which is the sum's low bits
+  static constexpr int MAGIC_BITS = 0x4B400000;
+  static __device__ __forceinline__ int whole(float q) { return __float_as_int(q + 12582912.f) - MAGIC_BITS; }
+
+  template <int N>
+  __device__ __forceinline__ void codes(const float (&x)[N], int (&c)[N]) const {
+    if (kind == GRID_FAST) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) c[i] = 0;
-  if (lo != lo || !(s <= 3.402823466e38f)) {
-    s = __uint_as_float(0x7FC00000u);
-    z = 0.f;
-    return false;
+      for (int i = 0; i < N; ++i)
+        c[i] = __vimin_s32_relu(__float_as_int(quotient(x[i], s, inv, low) + 12582912.f) + (zi - MAGIC_BITS), maxq);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        c[i] = kind == GRID_NAN ? 0 : int(fminf(fmaxf(rintf(__fdiv_rn(x[i], s)) + z, 0.f), float(maxq)));
+    }
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    c[i] = int(fminf(fmaxf(rintf(__fdiv_rn(x[i], s)) + z, 0.f), float(maxq)));
-  return true;
-}
+};
 
 // CTAs that an SM holds at once (measured on 131072 tokens of 8 x 128 bf16, grids, and 16384 of
 // 32 x 128 fp16, blocks: reads 4 / 6 / 8 at once 130 / 124 / 143 us for grids, whose spills
@@ -128,16 +143,22 @@ struct Resident {
 };
 constexpr int ROUNDS = 32;
 
+// Units of a lane in a write.  A group's range, grid and addresses cost a lane about as many
+// instructions as 16 codes do, and the kernel is bound by issuing them.
+template <int KIND>
+constexpr int LANE_UNITS = KIND == MX4 ? 1 : 2;
+
 template <typename T, int KIND>
 __global__ void __launch_bounds__(THREADS, Resident<KIND>::WRITE)
 k_cache_write(const Args a, int32_t* status) {
   using U = Unit<T>;
+  constexpr int LU = LANE_UNITS<KIND>, LN = LU * U::N;
   __shared__ Where stored[THREADS];
   const Place pl(a);
   const int64_t t0 = int64_t(blockIdx.x) * a.rows;
   const int rows = int(min(int64_t(a.rows), a.tokens - t0));
   const int group = pl.lane >> a.lane_bits;
-  const int first = pl.lane * U::N;                       // first value of the lane
+  const int first = pl.lane * LN;                         // first value of the lane
   const int n = pl.live ? a.dim - first : 0;
   const T* in = static_cast<const T*>(a.in[pl.kv]) + (t0 + pl.row) * a.ldt[pl.kv] +
                 pl.head * a.ldh[pl.kv] + first;
@@ -147,76 +168,90 @@ k_cache_write(const Args a, int32_t* status) {
   bool bad = false;
   // the next row is loading while one is quantised (one copy of that code: unrolled over the
   // rows it no longer fits the instruction cache; loading two ahead cost 6% for its registers)
-  U next;
-  next.load(in, pl.row < rows ? n : 0, a.vec != 0);
+  U next[LU];
+#pragma unroll
+  for (int u = 0; u < LU; ++u)
+    next[u].load(in + u * U::N, pl.row < rows ? n - u * U::N : 0, a.vec != 0);
   if (int(threadIdx.x) < rows) stored[threadIdx.x] = find_row(a, t0 + threadIdx.x, status);
   __syncthreads();
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += a.side) {
-    const U now = next;
+    U now[LU];
     const int r = r0 + pl.row;
     in += step;
-    next.load(in, r + a.side < rows ? n : 0, a.vec != 0);
-    {
-      Where at = {-1, 0};
-      if (r < rows && pl.live) at = stored[r];
-      uint32_t* codes = codes0 + at.word;
+#pragma unroll
+    for (int u = 0; u < LU; ++u) {
+      now[u] = next[u];
+      next[u].load(in + u * U::N, r + a.side < rows ? n - u * U::N : 0, a.vec != 0);
+    }
+    Where at = {-1, 0};
+    if (r < rows && pl.live) at = stored[r];
+    uint32_t* codes = codes0 + at.word;
+    if constexpr (KIND == MX4) {
       float v[U::N];
-      now.widen(v);
-      if constexpr (KIND == MX4) {
-        uint32_t m = now.amax_bits();
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        if (U::N == 8) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int e = mx::scale_byte(m);
-        const float f = mx::inv_scale(min(e, 253));
-        uint32_t w[U::WORDS];
+      now[0].widen(v);
+      uint32_t m = now[0].amax_bits();
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      if (U::N == 8) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = mx::scale_byte(m);
+      const float f = mx::inv_scale(min(e, 253));
+      uint32_t w[U::WORDS];
 #pragma unroll
-        for (int j = 0; j < U::N; ++j) v[j] *= f;
+      for (int j = 0; j < U::N; ++j) v[j] *= f;
 #pragma unroll
-        for (int j = 0; j < U::WORDS; ++j) w[j] = e == 255 ? 0u : mx::encode8(v + 8 * j);
-        if (at.word >= 0) {
-          bad |= e == 255;
-          if constexpr (U::WORDS == 2) *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
-          else *codes = w[0];
-          if ((first & 31) == 0)
-            static_cast<uint8_t*>(a.grids[pl.kv])[at.group + group0] = uint8_t(e);
-        }
-      } else {
-        constexpr int maxq = KIND == GRID4 ? 15 : 255;
-        float lo, hi;
-        now.range(lo, hi);
-        for (int o = 1; o < (1 << a.lane_bits); o <<= 1) {
-          lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-          hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        lo = min_nan(lo, 0.f);
-        hi = max_nan(hi, 0.f);
-        float sc, z;
-        int c[U::N];
-        const bool nan = !grid_codes<U::N, maxq>(v, lo, hi, a.sym, sc, z, c);
-        if (at.word >= 0 && n > 0) {
-          bad |= nan;
-          // 8 codes at a time: all of dim, which is a multiple of 8, and no more
-          if constexpr (KIND == GRID4) {
+      for (int j = 0; j < U::WORDS; ++j) w[j] = e == 255 ? 0u : mx::encode8(v + 8 * j);
+      if (at.word >= 0) {
+        bad |= e == 255;
+        if constexpr (U::WORDS == 2) *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
+        else *codes = w[0];
+        if ((first & 31) == 0)
+          static_cast<uint8_t*>(a.grids[pl.kv])[at.group + group0] = uint8_t(e);
+      }
+    } else {
+      constexpr int maxq = KIND == GRID4 ? 15 : 255;
+      float lo, hi;
+      now[0].range(lo, hi);
 #pragma unroll
-            for (int j = 0; j < U::WORDS; ++j) {
+      for (int u = 1; u < LU; ++u) {
+        float l, h;
+        now[u].range(l, h);
+        lo = min_nan(lo, l);
+        hi = max_nan(hi, h);
+      }
+      for (int o = 1; o < (1 << a.lane_bits); o <<= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      lo = min_nan(lo, 0.f);
+      hi = max_nan(hi, 0.f);
+      const Grid<maxq> g(lo, hi, a.sym);
+      if (at.word >= 0 && n > 0) {
+        bad |= g.kind == GRID_NAN;
+        // 8 codes at a time: all of dim, which is a multiple of 8, and no more
+#pragma unroll
+        for (int u = 0; u < LU; ++u) {
+          float v[U::N];
+          int c[U::N];
+          now[u].widen(v);
+          g.template codes<U::N>(v, c);
+#pragma unroll
+          for (int j = 0; j < U::WORDS; ++j) {
+            const int k = u * U::WORDS + j;              // eighth of the lane's values
+            if constexpr (KIND == GRID4) {
               uint32_t w = 0;
 #pragma unroll
               for (int i = 0; i < 8; ++i) w += uint32_t(c[8 * j + i]) << (4 * i);
-              if (8 * j < n) codes[j] = w;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < U::WORDS; ++j) {
+              if (8 * k < n) codes[k] = w;
+            } else {
               uint32_t w[2] = {0u, 0u};
 #pragma unroll
               for (int i = 0; i < 8; ++i) w[i >> 2] += uint32_t(c[8 * j + i]) << (8 * (i & 3));
-              if (8 * j < n) *reinterpret_cast<uint2*>(codes + 2 * j) = make_uint2(w[0], w[1]);
+              if (8 * k < n) *reinterpret_cast<uint2*>(codes + 2 * k) = make_uint2(w[0], w[1]);
             }
           }
-          if (pl.lane == group << a.lane_bits)
-            static_cast<float2*>(a.grids[pl.kv])[at.group + group0] = make_float2(sc, z);
         }
+        if (pl.lane == group << a.lane_bits)
+          static_cast<float2*>(a.grids[pl.kv])[at.group + group0] = make_float2(g.s, g.z);
       }
     }
   }
@@ -298,7 +333,8 @@ k_cache_read(const Args a, int32_t* status) {
 template <typename T, int KIND>
 gptq_status launch(cudaStream_t st, bool write, Args& a, int32_t* status) {
   if (write) {
-    const int per_group = KIND == MX4 ? 32 / Unit<T>::N : (a.group + Unit<T>::N - 1) / Unit<T>::N;
+    constexpr int LN = LANE_UNITS<KIND> * Unit<T>::N;
+    const int per_group = (a.group + LN - 1) / LN;
     while ((1 << a.lane_bits) < per_group) ++a.lane_bits;
     a.per_head = a.groups << a.lane_bits;
   } else {
