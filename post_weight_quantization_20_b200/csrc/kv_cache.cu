@@ -134,12 +134,12 @@ struct Grid {
   }
 };
 
-// CTAs that an SM holds at once (measured on 131072 tokens of 8 x 128 bf16, grids, and 16384 of
-// 32 x 128 fp16, blocks: reads 4 / 6 / 8 at once 130 / 124 / 143 us for grids, whose spills
-// start at 8, and 101 / 81 / 69 us for blocks), and the most rounds of rows of one
-template <int KIND>
+// CTAs that an SM holds at once, and the most rounds of rows of one.  Measured on 131072 tokens of
+// 8 x 128 bf16, grids, and 16384 of 32 x 128 fp16, blocks: reads 4 / 6 / 8 at once 130 / 124 / 143 us
+// for grids, whose spills start at 8 as those of fp32 blocks do, and 101 / 81 / 69 us for blocks.
+template <typename T, int KIND>
 struct Resident {
-  static constexpr int WRITE = KIND == MX4 ? 5 : 3, READ = KIND == MX4 ? 8 : 6;
+  static constexpr int WRITE = KIND == MX4 ? 5 : 3, READ = KIND == MX4 && sizeof(T) == 2 ? 8 : 6;
 };
 constexpr int ROUNDS = 32;
 
@@ -149,7 +149,7 @@ template <int KIND>
 constexpr int LANE_UNITS = KIND == MX4 ? 1 : 2;
 
 template <typename T, int KIND>
-__global__ void __launch_bounds__(THREADS, Resident<KIND>::WRITE)
+__global__ void __launch_bounds__(THREADS, Resident<T, KIND>::WRITE)
 k_cache_write(const Args a, int32_t* status) {
   using U = Unit<T>;
   constexpr int LU = LANE_UNITS<KIND>, LN = LU * U::N;
@@ -259,7 +259,7 @@ k_cache_write(const Args a, int32_t* status) {
 }
 
 template <typename T, int KIND>
-__global__ void __launch_bounds__(THREADS, Resident<KIND>::READ)
+__global__ void __launch_bounds__(THREADS, Resident<T, KIND>::READ)
 k_cache_read(const Args a, int32_t* status) {
   using O = Out<T>;
   __shared__ Where stored[THREADS];
@@ -276,7 +276,7 @@ k_cache_read(const Args a, int32_t* status) {
   __syncthreads();
   if (!pl.live) return;
   for (int r0 = pl.row; r0 < rows; r0 += STEPS * a.side) {
-    uint32_t w[STEPS][2];
+    uint32_t w[STEPS][2], e[STEPS];
     float2 g[STEPS];
     bool live[STEPS];
 #pragma unroll
@@ -295,7 +295,7 @@ k_cache_read(const Args a, int32_t* status) {
         w[s][0] = __ldg(p);
       }
       if constexpr (KIND == MX4)
-        g[s].x = mx::scale_value(__ldg(static_cast<const uint8_t*>(a.grids[pl.kv]) + at.group + group0));
+        e[s] = __ldg(static_cast<const uint8_t*>(a.grids[pl.kv]) + at.group + group0);
       else
         g[s] = __ldg(static_cast<const float2*>(a.grids[pl.kv]) + at.group + group0);
     }
@@ -306,9 +306,16 @@ k_cache_read(const Args a, int32_t* status) {
       // 4 fp32 values of a head are half a word of 4-bit codes
       if (KIND != GRID8 && O::N == 4) w[s][0] >>= 4 * (first & 4);
       if constexpr (KIND == MX4) {
+        // a scale that fp16 holds multiplies the levels there: both are exact, the product is
+        // rounded once
+        if (__is_same(T, __half) && a.vec && e[s] - 103u <= 39u) {
+          *reinterpret_cast<uint4*>(out + (r0 + s * a.side) * ldt) = mx::decode8_half(w[s][0], e[s]);
+          continue;
+        }
         mx::decode<O::N>(w[s][0], v);
+        const float f = mx::scale_value(e[s]);
 #pragma unroll
-        for (int j = 0; j < O::N; ++j) v[j] *= g[s].x;
+        for (int j = 0; j < O::N; ++j) v[j] *= f;
       } else {
         // the code as a float without a conversion: 2^23 + c (the code as the lowest byte of
         // that float), less 2^23 + z; both are whole numbers below 2^24 (z < 2^10 on any grid
@@ -349,7 +356,7 @@ gptq_status launch(cudaStream_t st, bool write, Args& a, int32_t* status) {
   // (a last wave that was three quarters full cost 15%)
   const int sms = sm_count();
   if (sms <= 0) return GPTQ_ERR_CUDA;
-  const int64_t slots = int64_t(sms) * (write ? Resident<KIND>::WRITE : Resident<KIND>::READ);
+  const int64_t slots = int64_t(sms) * (write ? Resident<T, KIND>::WRITE : Resident<T, KIND>::READ);
   const int64_t work = a.tokens * parts, most = std::min(THREADS / a.side, ROUNDS) * a.side;
   const int64_t waves = (work + slots * most - 1) / (slots * most);
   const int64_t even = (work + slots * waves - 1) / (slots * waves);

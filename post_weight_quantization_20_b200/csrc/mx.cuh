@@ -65,6 +65,26 @@ __device__ __forceinline__ void decode(uint32_t w, float (&v)[N]) {
   }
 }
 
+// The values of eight codes in fp16, for scales 2^-24 .. 2^15 (103 <= e <= 142).
+__device__ __forceinline__ uint4 decode8_half(uint32_t w, uint32_t e) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+  const __half2 f = __float2half2_rn(__uint_as_float(e << 23));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), f);
+    h[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
 // Byte offset of the scale of (row, block) in 128 x 4 tiles, `ct` tiles per tile row.
 __device__ __forceinline__ int64_t scale_offset(int64_t row, int block, int ct) {
   return ((row >> 7) * ct + (block >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +

@@ -204,6 +204,26 @@ def test_rounding_near_ties_takes_the_exact_quotient():
     np.testing.assert_array_equal(c.view(np.uint32), words)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_read_every_code_and_scale(dtype):
+    # formed in fp32 (6 * 2^127 overflows there), then rounded once
+    codes = np.tile(np.arange(16, dtype=np.uint8), (256, 2))
+    e = np.arange(256, dtype=np.uint8)[:, None]
+    cfg = KV.make_cache_config("mx")
+    pool = KV.KVCache.alloc(cfg, 1, 256, 1, 32)
+    for c, g in ((pool.k_codes, pool.k_grids), (pool.v_codes, pool.v_grids)):
+        c.copy_(torch.from_numpy(o.pack(codes.astype(np.int64), 4).view(np.int32)).reshape(c.shape))
+        g.copy_(torch.from_numpy(e).reshape(g.shape))
+    i32 = dict(dtype=torch.int32, device=DEV)
+    K, V = pool.read(torch.zeros(1, 1, **i32), torch.tensor([0, 256], **i32), torch.zeros(1, **i32),
+                     256, dtype)
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(L.mx_values(codes, e).astype(np.float32)).to(dtype)[:, None]
+    for got in (K.cpu(), V.cpu()):
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0))
+
+
 def test_bad_positions_and_pages_are_left_out():
     # negative starts, positions past the table, pages that do not exist: those rows are left
     # out and reported, the others are done
