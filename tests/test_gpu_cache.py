@@ -351,3 +351,45 @@ def test_two_caches_on_two_streams():
         want = _define(x.double().cpu().numpy(), *conf)[2]
         np.testing.assert_array_equal(K.cpu().numpy(), want)
         np.testing.assert_array_equal(V.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("conf", [CONFIGS[4], CONFIGS[7]], ids=lambda c: "-".join(map(str, c)))
+def test_a_layer_runs_from_activations_to_the_cache_and_back(conf):
+    # prompts, then single tokens: activations are quantised, multiplied by 4-bit weights into
+    # keys and values beside the queries, appended where they lie and read back; every step
+    # equals the definitions applied to what it was given
+    from post_weight_quantization_20_b200 import mx as MX
+    heads, dim, cols, page = 2, 64, 1000, 16
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    w = MX.mx_quantize(torch.randn(6 * heads * dim // 2, cols, generator=gen, device=DEV).half() * 0.03)
+    wv = L.mx_values(*L.mx_quantize(MX.mx_dequantize(w).double().cpu().numpy()))[:, :cols]
+    cfg = KV.make_cache_config(*conf)
+    lens = [20, 5, 33]
+    call = Call([n + 4 for n in lens], [0, 0, 0], page, 3)
+    table = torch.from_numpy(call.table).to(DEV)
+    cache = KV.KVCache.alloc(cfg, call.pages, page, heads, dim)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    kept = [[], [], []]
+    have = [0, 0, 0]
+    for step in range(5):
+        new = lens if step == 0 else [1, 1, 1]
+        X = torch.randn(sum(new), cols, generator=gen, device=DEV).bfloat16()
+        Y = MX.mx_linear(X, w)                                   # (rows, (q, k, v) heads * dim)
+        qx = L.mx_values(*L.mx_quantize(X.double().cpu().numpy()))[:, :cols]
+        want, S = qx @ wv.T, np.abs(qx) @ np.abs(wv).T
+        bound = 50 * 2.0 ** -23 * S
+        bound = bound + 2.0 ** -8 * (np.abs(want) + bound)       # rounded to bf16: half a step
+        assert np.all(np.abs(Y.double().cpu().numpy() - want) <= bound)
+        K, V = Y.view(len(Y), 3, heads, dim)[:, 1], Y.view(len(Y), 3, heads, dim)[:, 2]
+        cu = torch.tensor([0, *np.cumsum(new)], **i32)
+        cache.write(K, V, table, cu, torch.tensor(have, **i32))
+        at = 0
+        for s, n in enumerate(new):
+            kept[s].append((K[at:at + n].double().cpu().numpy(), V[at:at + n].double().cpu().numpy()))
+            at += n
+            have[s] += n
+        total = torch.tensor([0, *np.cumsum(have)], **i32)
+        k, v = cache.read(table, total, torch.zeros(3, **i32), sum(have), torch.float32)
+        for got, i in ((k, 0), (v, 1)):
+            rows = np.concatenate([r[i] for s in kept for r in s])
+            np.testing.assert_array_equal(got.cpu().numpy(), _define(rows, *conf)[2])

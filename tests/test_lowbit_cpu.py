@@ -307,3 +307,35 @@ def test_grid_definition_matches_the_weight_grid_and_its_edges():
     c, s, z = L.grid_quantize(edge, 4, 0, False)
     v = L.grid_values(c, s, z, 0)
     assert (v[0] == 0).all() and np.isnan(v[1]).all() and np.isnan(v[2]).all() and (v[3] == 0).all()
+
+
+def test_calls_run_on_their_tensors_device_and_current_stream(monkeypatch):
+    # tensors of a device that is not the current one: that device is made current for the
+    # launch, and its own current stream is taken, not the other device's
+    import contextlib
+    seen = []
+
+    @contextlib.contextmanager
+    def device(d):
+        seen.append(("enter", d))
+        yield
+        seen.append(("leave", d))
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    MX._call(lambda *a: seen.append(a) or 0, "f", 0, None, "x")
+    assert seen == [("enter", 0), ("x", 1000), ("leave", 0)]
+    seen.clear()
+    MX._call(lambda *a: seen.append(a) or 0, "f", 1, None, "x")
+    assert seen == [("x", 1001)]
+    seen.clear()
+
+    class Stream:
+        cuda_stream = 77
+
+    MX._call(lambda *a: seen.append(a) or 0, "f", 1, Stream(), "x")
+    assert seen == [("x", 77)]
+    with pytest.raises(G.GPTQError) as e:
+        MX._call(lambda *a: G.GPTQ_ERR_UNSUPPORTED, "f", 1, None)
+    assert e.value.code == G.GPTQ_ERR_UNSUPPORTED
