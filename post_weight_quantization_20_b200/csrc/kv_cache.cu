@@ -154,7 +154,9 @@ k_cache_write(const Args a, int32_t* status) {
   using U = Unit<T>;
   constexpr int LU = LANE_UNITS<KIND>, LN = LU * U::N;
   __shared__ Where stored[THREADS];
+  allow_successor();
   const Place pl(a);
+  wait_for_predecessor();
   const int64_t t0 = int64_t(blockIdx.x) * a.rows;
   const int rows = int(min(int64_t(a.rows), a.tokens - t0));
   const int group = pl.lane >> a.lane_bits;
@@ -263,7 +265,9 @@ __global__ void __launch_bounds__(THREADS, Resident<T, KIND>::READ)
 k_cache_read(const Args a, int32_t* status) {
   using O = Out<T>;
   __shared__ Where stored[THREADS];
+  allow_successor();
   const Place pl(a);
+  wait_for_predecessor();
   const int64_t t0 = int64_t(blockIdx.x) * a.rows;
   const int rows = int(min(int64_t(a.rows), a.tokens - t0));
   if (int(threadIdx.x) < rows) stored[threadIdx.x] = find_row(a, t0 + threadIdx.x, status);
@@ -288,16 +292,16 @@ k_cache_read(const Args a, int32_t* status) {
       if (!live[s]) continue;
       const uint32_t* p = codes + at.word;
       if constexpr (KIND == GRID8 && O::N == 8) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
         w[s][0] = q.x;
         w[s][1] = q.y;
       } else {
-        w[s][0] = __ldg(p);
+        w[s][0] = *p;
       }
       if constexpr (KIND == MX4)
-        e[s] = __ldg(static_cast<const uint8_t*>(a.grids[pl.kv]) + at.group + group0);
+        e[s] = static_cast<const uint8_t*>(a.grids[pl.kv])[at.group + group0];
       else
-        g[s] = __ldg(static_cast<const float2*>(a.grids[pl.kv]) + at.group + group0);
+        g[s] = static_cast<const float2*>(a.grids[pl.kv])[at.group + group0];
     }
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -363,8 +367,8 @@ gptq_status launch(cudaStream_t st, bool write, Args& a, int32_t* status) {
   a.rows = int((even + a.side - 1) / a.side * a.side);
   const int64_t blocks = (a.tokens + a.rows - 1) / a.rows;
   const dim3 grid{unsigned(blocks), unsigned(parts)};
-  if (write) GPTQ_LAUNCH((k_cache_write<T, KIND>), grid, THREADS, 0, st, a, status);
-  else GPTQ_LAUNCH((k_cache_read<T, KIND>), grid, THREADS, 0, st, a, status);
+  if (write) GPTQ_LAUNCH_EARLY((k_cache_write<T, KIND>), grid, THREADS, st, a, status);
+  else GPTQ_LAUNCH_EARLY((k_cache_read<T, KIND>), grid, THREADS, st, a, status);
   return GPTQ_OK;
 }
 

@@ -48,12 +48,14 @@ struct Item {
 
 template <typename T, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(WARPS * 32)
-k_mx_quantize(const T* __restrict__ X, int64_t ldx, const Walk w, uint32_t* __restrict__ codes,
-              uint8_t* __restrict__ scales, int32_t* status) {
+k_mx_quantize(const T* X, int64_t ldx, const Walk w, uint32_t* codes,
+              uint8_t* scales, int32_t* status) {
   using U = Unit<T>;
   constexpr int STEPS = sizeof(T) == 4 ? 4 : 2;
+  allow_successor();
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+  wait_for_predecessor();
   if (item >= w.items) return;
   const Item<U::N, STEPS, WIDE> it(w, item, lane);
   const int nb = (w.cols + 31) >> 5, ct = (nb + 3) >> 2;
@@ -110,12 +112,14 @@ k_mx_quantize(const T* __restrict__ X, int64_t ldx, const Walk w, uint32_t* __re
 // codes straddle two words and perhaps two blocks, and its store is whole all the same.
 template <typename T, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(WARPS * 32)
-k_mx_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, const Walk w,
-                T* __restrict__ Y, int64_t ldy) {
+k_mx_dequantize(const uint32_t* codes, const uint8_t* scales, const Walk w,
+                T* Y, int64_t ldy) {
   using O = Out<T>;
   constexpr int STEPS = 4;
+  allow_successor();
   const int lane = threadIdx.x & 31;
   const int64_t item = int64_t(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+  wait_for_predecessor();
   if (item >= w.items) return;
   const Item<O::N, STEPS, WIDE> it(w, item, lane);
   const int nb = (w.cols + 31) >> 5, ct = (nb + 3) >> 2;
@@ -133,18 +137,18 @@ k_mx_dequantize(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ 
       const uint32_t* p = codes + row * (4 * int64_t(nb));
       if (VEC) {
         if (c < w.cols) {
-          q[s] = __ldg(p + (c >> 3));
-          e[s] = __ldg(scales + mx::scale_offset(row, c >> 5, ct));
+          q[s] = p[c >> 3];
+          e[s] = scales[mx::scale_offset(row, c >> 5, ct)];
         }
       } else {
         const int last = c + O::N - 1;
         if (c >= 0 && c < w.cols) {
-          q[s] = __ldg(p + (c >> 3));
-          e[s] = __ldg(scales + mx::scale_offset(row, c >> 5, ct));
+          q[s] = p[c >> 3];
+          e[s] = scales[mx::scale_offset(row, c >> 5, ct)];
         }
         if (last >= 0 && last < 32 * nb) {
-          q1[s] = __ldg(p + (last >> 3));
-          e1[s] = __ldg(scales + mx::scale_offset(row, last >> 5, ct));
+          q1[s] = p[last >> 3];
+          e1[s] = scales[mx::scale_offset(row, last >> 5, ct)];
         }
       }
     }
@@ -201,9 +205,9 @@ gptq_status quantize_v(cudaStream_t st, const T* x, int64_t ldx, const Walk& w, 
                        uint8_t* scales, int32_t* status) {
   const unsigned blocks = unsigned((w.items + WARPS - 1) / WARPS);
   if (w.lane_bits == 5)
-    GPTQ_LAUNCH((k_mx_quantize<T, VEC, true>), blocks, WARPS * 32, 0, st, x, ldx, w, codes, scales, status);
+    GPTQ_LAUNCH_EARLY((k_mx_quantize<T, VEC, true>), blocks, WARPS * 32, st, x, ldx, w, codes, scales, status);
   else
-    GPTQ_LAUNCH((k_mx_quantize<T, VEC, false>), blocks, WARPS * 32, 0, st, x, ldx, w, codes, scales, status);
+    GPTQ_LAUNCH_EARLY((k_mx_quantize<T, VEC, false>), blocks, WARPS * 32, st, x, ldx, w, codes, scales, status);
   return GPTQ_OK;
 }
 
@@ -212,9 +216,9 @@ gptq_status dequantize_v(cudaStream_t st, const uint32_t* codes, const uint8_t* 
                          T* y, int64_t ldy) {
   const unsigned blocks = unsigned((w.items + WARPS - 1) / WARPS);
   if (w.lane_bits == 5)
-    GPTQ_LAUNCH((k_mx_dequantize<T, VEC, true>), blocks, WARPS * 32, 0, st, codes, scales, w, y, ldy);
+    GPTQ_LAUNCH_EARLY((k_mx_dequantize<T, VEC, true>), blocks, WARPS * 32, st, codes, scales, w, y, ldy);
   else
-    GPTQ_LAUNCH((k_mx_dequantize<T, VEC, false>), blocks, WARPS * 32, 0, st, codes, scales, w, y, ldy);
+    GPTQ_LAUNCH_EARLY((k_mx_dequantize<T, VEC, false>), blocks, WARPS * 32, st, codes, scales, w, y, ldy);
   return GPTQ_OK;
 }
 

@@ -124,8 +124,8 @@ struct Unit {
   __device__ __forceinline__ void load(const T* p, int n, bool vec) {
     q[0] = q[1] = make_uint4(0u, 0u, 0u, 0u);
     if (vec && n >= N / 2) {
-      q[0] = __ldg(reinterpret_cast<const uint4*>(p));
-      if (n >= N) q[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+      q[0] = *reinterpret_cast<const uint4*>(p);
+      if (n >= N) q[1] = reinterpret_cast<const uint4*>(p)[1];
       else set_some(p, N / 2, n);
     } else {
       set_some(p, 0, n);
@@ -150,9 +150,9 @@ struct Unit {
     q2 = make_uint4(0u, 0u, 0u, 0u);
     if (whole) {
       const uint4* g = reinterpret_cast<const uint4*>(at);
-      q[0] = __ldg(g);
-      q[1] = __ldg(g + 1);
-      q2 = __ldg(g + 2);
+      q[0] = g[0];
+      q[1] = g[1];
+      q2 = g[2];
     } else {
       q[0] = q[1] = q2;
       set_some(p, 0, n);

@@ -120,6 +120,8 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
   const uint32_t tmem_base = *tmem_slot;
   int64_t issued = 0;
 
+  allow_successor();
+  wait_for_predecessor();
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0;
@@ -389,6 +391,8 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                                                       cluster_scope));
   };
 
+  allow_successor();
+  wait_for_predecessor();
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0;
@@ -630,17 +634,18 @@ int64_t clusters_at_once(int ctas, int sms) {
 }
 
 cudaLaunchConfig_t cluster_launch(unsigned x, unsigned y, int cluster, int threads, int smem,
-                                  cudaStream_t st, cudaLaunchAttribute& at) {
+                                  cudaStream_t st, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(x, y);
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = st;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = unsigned(cluster);
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(cluster);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1] = may_start_early();
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -658,7 +663,7 @@ gptq_status launch_few(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, 
          p.boxes >= 2 * C::SUB * splits)
     splits *= 2;
   GPTQ_CUDA(allow_smem(k_mx_few<BN, T>, C::SMEM));
-  cudaLaunchAttribute at;
+  cudaLaunchAttribute at[2];
   const cudaLaunchConfig_t cfg = cluster_launch(unsigned(rows * splits), unsigned(cols), splits,
                                                 FEW_THREADS, C::SMEM, st, at);
   GPTQ_CUDA(cudaLaunchKernelEx(&cfg, k_mx_few<BN, T>, wmap, xmap, p, status));
@@ -677,7 +682,7 @@ gptq_status launch_pair(cudaStream_t st, const uint32_t* xc, const uint32_t* wc,
     return GPTQ_ERR_UNSUPPORTED;
   GPTQ_CUDA(allow_smem(pair::k_mx_pair<T>, pair::SMEM));
   const int clusters = int(std::min<int64_t>(sms / (2 * splits), int64_t(p.ntr) * p.ntt));
-  cudaLaunchAttribute at;
+  cudaLaunchAttribute at[2];
   const cudaLaunchConfig_t cfg = cluster_launch(unsigned(2 * splits * clusters), 1, 2 * splits,
                                                 pair::THREADS, pair::SMEM, st, at);
   GPTQ_CUDA(cudaLaunchKernelEx(&cfg, pair::k_mx_pair<T>, wmap, xmap, wsmap, xsmap, p,

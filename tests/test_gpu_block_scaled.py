@@ -260,6 +260,36 @@ def test_product_repeats_bit_for_bit_and_on_two_streams():
         assert torch.equal(y, ref)
 
 
+@pytest.mark.parametrize("M,R,C", [(3, 300, 700), (150, 700, 1000), (2000, 300, 4000)])
+def test_calls_back_to_back_see_each_others_results(M, R, C):
+    # each call starts while the one before it drains; one pair of buffers is rewritten again and
+    # again, so a read of anything but the latest contents shows
+    X = [torch.randn(M, C, device=DEV).half() for _ in range(3)]
+    w = MX.mx_quantize(torch.randn(R, C, device=DEV))
+    q = MX.mx_quantize(X[0])
+    want = []
+    for x in X:
+        one = MX.mx_quantize(x)
+        torch.cuda.synchronize()
+        want.append((MX.mx_dequantize(one, torch.float16), MX.mx_matmul(one, w)))
+        torch.cuda.synchronize()
+    n = 30
+    out = torch.empty(n, M, C, dtype=torch.float16, device=DEV)
+    Y = torch.empty(n, M, R, device=DEV)
+    torch.cuda.synchronize()
+    for i in range(n):
+        MX.gptq_mx_quantize(X[i % 3], q.codes, q.scales)
+        if i % 2:
+            MX.gptq_mx_dequantize(q.codes, q.scales, out[i])
+            MX.gptq_mx_matmul(q.codes, q.scales, w.codes, w.scales, C, Y[i])
+        else:
+            MX.gptq_mx_matmul(q.codes, q.scales, w.codes, w.scales, C, Y[i])
+            MX.gptq_mx_dequantize(q.codes, q.scales, out[i])
+    torch.cuda.synchronize()
+    for i in range(n):
+        assert torch.equal(out[i], want[i % 3][0]) and torch.equal(Y[i], want[i % 3][1]), i
+
+
 @pytest.mark.parametrize("M,R,C", [(4, 700, 1000), (300, 600, 2000)])
 def test_graph_replay_sees_new_inputs(M, R, C):
     X = torch.randn(M, C, device=DEV)

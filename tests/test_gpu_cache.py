@@ -332,6 +332,31 @@ def test_graph_replay_with_growing_sequences():
         np.testing.assert_array_equal(V[:2 * step + 2].cpu().numpy(), -want)
 
 
+@pytest.mark.parametrize("rows", [2, 300, 6000])
+def test_calls_back_to_back_see_each_others_results(rows):
+    # each call starts while the one before it drains; the same slots are rewritten again and again
+    call = Call([rows], [3], 16, 1)
+    cfg = KV.make_cache_config("grid", 4, 64)
+    pool = KV.KVCache.alloc(cfg, call.pages, 16, 8, 128)
+    args = call.args()
+    xs = [_input(rows, 8, 128, torch.bfloat16, i).to(DEV) for i in range(3)]
+    want, negs = [], [-x for x in xs]
+    for x in xs:
+        pool.write(x, -x, *args)
+        torch.cuda.synchronize()
+        want.append(pool.read(*args, rows, torch.float32))
+        torch.cuda.synchronize()
+    outs = [[torch.zeros(rows, 8, 128, device=DEV) for _ in range(2)] for _ in range(20)]
+    arrays = (pool.k_codes, pool.k_grids, pool.v_codes, pool.v_grids)
+    torch.cuda.synchronize()
+    for i, o2 in enumerate(outs):
+        KV.gptq_cache_write(xs[i % 3], negs[i % 3], cfg, *arrays, *args)
+        KV.gptq_cache_read(cfg, *arrays, *args, *o2)
+    torch.cuda.synchronize()
+    for i, (K, V) in enumerate(outs):
+        assert torch.equal(K, want[i % 3][0]) and torch.equal(V, want[i % 3][1]), i
+
+
 def test_two_caches_on_two_streams():
     call = Call([50, 30], [0, 0], 16, 7)
     pools, xs = [], []
