@@ -15,6 +15,7 @@ non-finite groups are reported in `status`, as the header says.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -33,18 +34,10 @@ class gptq_cache_config(ctypes.Structure):
                 ("sym", ctypes.c_int)]
 
 
-class gptq_cache(ctypes.Structure):
-    _fields_ = [("k_codes", ctypes.c_void_p), ("k_grids", ctypes.c_void_p),
-                ("v_codes", ctypes.c_void_p), ("v_grids", ctypes.c_void_p),
-                ("pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
-                ("heads", ctypes.c_int64), ("dim", ctypes.c_int64)]
-
-
-class gptq_cache_rows(ctypes.Structure):
-    _fields_ = [("table", ctypes.c_void_p), ("table_ld", ctypes.c_int64),
-                ("width", ctypes.c_int64), ("cu", ctypes.c_void_p), ("start", ctypes.c_void_p),
-                ("seqs", ctypes.c_int64)]
-
+# struct gptq_cache and struct gptq_cache_rows of the header, packed per call (a ctypes.Structure
+# costs the host three times as much to make)
+_CACHE = struct.Struct("@4P4q")
+_ROWS = struct.Struct("@PqqPPq")
 
 _lib = None
 
@@ -55,8 +48,7 @@ def load_library() -> ctypes.CDLL:
     if _lib is None:
         lib = G.load_library()
         vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
-        cfg, cache, rows = (ctypes.POINTER(t) for t in (gptq_cache_config, gptq_cache,
-                                                        gptq_cache_rows))
+        cfg, cache, rows = ctypes.POINTER(gptq_cache_config), ctypes.c_char_p, ctypes.c_char_p
         for name in ("gptq_cache_words", "gptq_cache_grid_bytes"):
             getattr(lib, name).argtypes = [cfg, i64]
             getattr(lib, name).restype = ctypes.c_size_t
@@ -176,10 +168,10 @@ def _marshal(K, V, cfg, k_codes, k_grids, v_codes, v_grids, table, cu, start, st
             == v_codes.get_device() == v_grids.get_device() == table.get_device()
             == cu.get_device() == start.get_device()):
         G._need_cuda(K, V, k_codes, k_grids, v_codes, v_grids, table, cu, start, status)
-    cache = gptq_cache(k_codes.data_ptr(), k_grids.data_ptr(), v_codes.data_ptr(),
-                       v_grids.data_ptr(), pages, page_size, H, D)
-    rows = gptq_cache_rows(table.data_ptr(), ld, width, cu.data_ptr(), start.data_ptr(), S)
-    where = (ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rows))
+    where = (ctypes.byref(cfg),
+             _CACHE.pack(k_codes.data_ptr(), k_grids.data_ptr(), v_codes.data_ptr(),
+                         v_grids.data_ptr(), pages, page_size, H, D),
+             _ROWS.pack(table.data_ptr(), ld, width, cu.data_ptr(), start.data_ptr(), S))
     data = (K.data_ptr(), V.data_ptr(), G._DT[K.dtype], T, kt, kh, vt, vh)
     return dev, where, data, st
 

@@ -39,8 +39,12 @@ def test_headers_compile_as_c99(tmp_path):
     if cc is None:
         pytest.skip("no C compiler")
     src = tmp_path / "t.c"
-    src.write_text('#include "gptq_mx.h"\n#include "gptq_cache.h"\n'
+    # and the structures lie in memory as the binding packs them
+    src.write_text('#include <stddef.h>\n#include "gptq_mx.h"\n#include "gptq_cache.h"\n'
                    "int main(void) { gptq_cache_config c = {GPTQ_CACHE_GRID, 8, 0, 0};\n"
+                   f"  if (sizeof(gptq_cache) != {KV._CACHE.size} || offsetof(gptq_cache, dim) != 56 ||\n"
+                   f"      sizeof(gptq_cache_rows) != {KV._ROWS.size} || offsetof(gptq_cache_rows, cu) != 24)\n"
+                   "    return 2;\n"
                    "  return gptq_mx_scale_bytes(1, 1) == 512 && gptq_cache_words(&c, 64) == 16 ? 0 : 1; }\n")
     libdir = os.path.dirname(G.LIB_PATH)
     MX.load_library()
@@ -110,15 +114,16 @@ def _cache_args(cfg=None, **over):
     a = dict(K=FAKE, V=FAKE, dt=1, tokens=3)
     for k, v in over.items():
         next(d for d in (c, r, a) if k in d)[k] = v
-    return a, cfg or KV.make_cache_config("grid", 4, 32), KV.gptq_cache(**c), KV.gptq_cache_rows(**r)
+    null = lambda d: [v or 0 for v in d.values()]  # noqa: E731
+    return a, cfg or KV.make_cache_config("grid", 4, 32), KV._CACHE.pack(*null(c)), KV._ROWS.pack(*null(r))
 
 
 def _cache_calls(cfg=None, **over):
     a, cfg, c, r = _cache_args(cfg, **over)
     lib, ref = KV.load_library(), ctypes.byref
     st = (128, 64, 128, 64)
-    w = lib.gptq_cache_write(a["K"], a["V"], a["dt"], a["tokens"], *st, ref(cfg), ref(c), ref(r), None, None)
-    d = lib.gptq_cache_read(ref(cfg), ref(c), ref(r), a["K"], a["V"], a["dt"], a["tokens"], *st, None, None)
+    w = lib.gptq_cache_write(a["K"], a["V"], a["dt"], a["tokens"], *st, ref(cfg), c, r, None, None)
+    d = lib.gptq_cache_read(ref(cfg), c, r, a["K"], a["V"], a["dt"], a["tokens"], *st, None, None)
     assert w == d
     return w
 
