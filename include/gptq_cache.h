@@ -32,12 +32,13 @@
  * cu[seqs]) are padding: a write ignores them and a read leaves them as they are.  A row whose position or page
  * is out of range (start < 0, p / page_size >= width, a page outside 0 .. pages-1) is left
  * out as well and raises GPTQ_ERR_INVALID_ARG in *dev_status; the other rows are done.
- * Two rows of one write must not have the same slot: which of them is stored, group by
- * group, is then not defined (pages shared by sequences may be read, not written).
+ * Two rows of one write must not have the same slot: what that slot holds is then not
+ * defined (pages shared by sequences may be read, not written).
  *
  * Conventions are those of gptq.h.  A call launches at most one kernel, keeps no state,
  * needs no workspace and may be captured into a CUDA graph; cu, start and table are read
- * on the device when it runs.
+ * on the device when it runs.  A kernel may start while the call before it on the same
+ * stream drains; it waits for that one's end before it touches memory.
  */
 #ifndef GPTQ_CACHE_H_
 #define GPTQ_CACHE_H_

@@ -23,7 +23,9 @@
  *
  * Conventions (ownership, streams, status codes, device conditions) are those of gptq.h.
  * Every call launches at most one kernel, keeps no state and needs no workspace; results
- * do not depend on timing.  The calls may be captured into a CUDA graph.
+ * do not depend on timing.  The calls may be captured into a CUDA graph.  A kernel may start
+ * while the call before it on the same stream drains; it waits for that one's end before it
+ * touches memory, so the order of the stream holds.
  */
 #ifndef GPTQ_MX_H_
 #define GPTQ_MX_H_
@@ -65,7 +67,7 @@ gptq_status gptq_mx_dequantize(const uint32_t* codes, const uint8_t* scales, int
  * Products are exact, sums are held in fp32 and rounded once to ydtype.  Any m_tokens, rows
  * >= 0 (0: a no-op) and cols >= 1; one token is as good a case as many.  A block of either
  * side with e = 255 makes the outputs of its row NaN.  Device conditions: TIMEOUT.
- * Errors: INVALID_ARG, UNSUPPORTED (no device with these tensor cores).
+ * Errors: INVALID_ARG, UNSUPPORTED (the driver cannot encode the operands' tensor maps).
  */
 gptq_status gptq_mx_matmul(const uint32_t* x_codes, const uint8_t* x_scales, int64_t m_tokens,
                            const uint32_t* w_codes, const uint8_t* w_scales, int64_t rows,

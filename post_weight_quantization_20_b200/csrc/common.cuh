@@ -90,16 +90,23 @@ inline cudaError_t allow_smem(K kernel, int bytes) {
     }                                                                       \
   } while (0)
 
-// The same for a kernel that begins with wait_for_predecessor() (no dynamic shared memory).
-#define GPTQ_LAUNCH_EARLY(kernel, grid, block, stream, ...)                          \
-  do {                                                                               \
-    const cudaError_t e_ = ::gptq::launch_early(kernel, grid, block, stream, __VA_ARGS__); \
-    ::gptq::note_launch();                                                           \
-    if (e_ != cudaSuccess) {                                                         \
-      ::gptq::note_error(e_, #kernel);                                               \
-      return GPTQ_ERR_CUDA;                                                          \
-    }                                                                                \
+// Count a launch that `call` (cudaLaunchKernelEx) made, or turn its error into GPTQ_ERR_CUDA and
+// clear it, so that the next launch is not blamed for it.
+#define GPTQ_LAUNCHED(call, name)                                           \
+  do {                                                                      \
+    const cudaError_t e_ = (call);                                          \
+    if (e_ != cudaSuccess) {                                                \
+      (void)cudaGetLastError();                                             \
+      ::gptq::note_error(e_, name);                                         \
+      return GPTQ_ERR_CUDA;                                                 \
+    }                                                                       \
+    ::gptq::note_launch();                                                  \
   } while (0)
+
+// A launch that may start early: of a kernel that calls wait_for_predecessor() (no dynamic
+// shared memory).
+#define GPTQ_LAUNCH_EARLY(kernel, grid, block, stream, ...) \
+  GPTQ_LAUNCHED(::gptq::launch_early(kernel, grid, block, stream, __VA_ARGS__), #kernel)
 
 #define GPTQ_CUDA(call)                                                     \
   do {                                                                      \

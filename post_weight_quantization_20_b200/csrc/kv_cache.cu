@@ -312,9 +312,11 @@ k_cache_read(const Args a, int32_t* status) {
       if constexpr (KIND == MX4) {
         // a scale that fp16 holds multiplies the levels there: both are exact, the product is
         // rounded once
-        if (__is_same(T, __half) && a.vec && e[s] - 103u <= 39u) {
-          *reinterpret_cast<uint4*>(out + (r0 + s * a.side) * ldt) = mx::decode8_half(w[s][0], e[s]);
-          continue;
+        if constexpr (__is_same(T, __half)) {
+          if (a.vec && e[s] - 103u <= 39u) {
+            *reinterpret_cast<uint4*>(out + (r0 + s * a.side) * ldt) = mx::decode8_half(w[s][0], e[s]);
+            continue;
+          }
         }
         mx::decode<O::N>(w[s][0], v);
         const float f = mx::scale_value(e[s]);

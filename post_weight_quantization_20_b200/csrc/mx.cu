@@ -3,7 +3,7 @@
 // Both are one pass over the data, bound by HBM: 2 or 4 bytes per element on one side,
 // 4.25 bits on the other.  A lane holds 32 bytes of a row to quantise (a block's maximum is
 // one or two shuffles), or writes 16 bytes read back; a warp's steps are loaded together.
-// Rows that are narrower than a warp's step share it, lanes_bits lanes to a row.
+// Rows that are narrower than a warp's step share it, 2^lane_bits lanes to a row.
 // Rows that do not start on 16-byte boundaries are still read and written in whole 16-byte
 // granules, their bytes or codes shifted into place: element by element they took 6 to 7 times
 // as long (20000 x 11003 bf16 read back: 609 us; through shared memory 236 us).

@@ -74,6 +74,7 @@ struct Few {
   static_assert(COLS <= 512 && BN * 512 <= STAGES * STAGE, "TMEM, partial sums");
 };
 
+// BN: the token tile, all of the M <= BN tokens
 template <int BN, typename T>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
 k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -92,7 +93,7 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int split = int(tc::cluster_rank()), splits = int(tc::cluster_size());
   const int rt = blockIdx.x / splits;
-  const int r0 = rt * 128, n0 = blockIdx.y * BN;
+  const int r0 = rt * 128;
   const int b0 = int(int64_t(p.boxes) * split / splits);
   const int b1 = int(int64_t(p.boxes) * (split + 1) / splits);
 
@@ -139,9 +140,8 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
           tc::tma_load_2d(a + j * A_BOX, &wmap, (b + j) * KB, r0, full + stage);
         tc::bulk_load(s, p.ws + (int64_t(rt) * p.ct + 2 * b) * 512, sb, full + stage);
         for (int j = 0; j < nbx; ++j)
-          tc::tma_load_2d(x + j * C::B_BOX, &xmap, (b + j) * KB, n0, full + stage);
-        tc::bulk_load(s + C::SUB * C::S_BOX, p.xs + (int64_t(n0 / 128) * p.ct + 2 * b) * 512, sb,
-                      full + stage);
+          tc::tma_load_2d(x + j * C::B_BOX, &xmap, (b + j) * KB, 0, full + stage);
+        tc::bulk_load(s + C::SUB * C::S_BOX, p.xs + int64_t(2 * b) * 512, sb, full + stage);
       }
       __syncwarp();
       ++issued;
@@ -193,16 +193,15 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
     if (tc::mbar_wait(acc_full, 0, abort_flag, p.wait_limit)) {
       tc::fence_after_sync();
       float* part = reinterpret_cast<float*>(smem);      // [token][128 rows]; the ring is empty
-      const int live = min(BN, p.M - n0);
-      for (int c = 0; c < live; c += 16) {
+      for (int c = 0; c < p.M; c += 16) {
         uint32_t v[16];
         tc::tmem_ld_32x16(tmem_base + (uint32_t(lane_base) << 16) + uint32_t(c), v);
         tc::tmem_ld_wait();
         if (splits == 1) {
-          T* y = static_cast<T*>(p.Y) + int64_t(n0 + c) * p.ldy + row;
+          T* y = static_cast<T*>(p.Y) + int64_t(c) * p.ldy + row;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (row < p.R && c + i < live) y[i * p.ldy] = from_f32<T>(__uint_as_float(v[i]));
+            if (row < p.R && c + i < p.M) y[i * p.ldy] = from_f32<T>(__uint_as_float(v[i]));
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) part[(c + i) * 128 + lane_base + lane] = __uint_as_float(v[i]);
@@ -216,8 +215,8 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
     // every CTA of the cluster sums its share of the tokens, the splits in order
     tc::cluster_sync();
     // (a warp a token, a lane four layer rows, all loads before the first sum)
-    const int live = min(BN, p.M - n0), row = r0 + 4 * lane;
-    for (int t = split + splits * warp; t < live; t += splits * (FEW_THREADS / 32)) {
+    const int row = r0 + 4 * lane;
+    for (int t = split + splits * warp; t < p.M; t += splits * (FEW_THREADS / 32)) {
       const uint32_t at = tc::smem_u32(smem + (t * 128 + 4 * lane) * 4);
       float4 part[8];
 #pragma unroll
@@ -232,7 +231,7 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
           v.z += part[q].z;
           v.w += part[q].w;
         }
-      T* y = static_cast<T*>(p.Y) + int64_t(n0 + t) * p.ldy + row;
+      T* y = static_cast<T*>(p.Y) + int64_t(t) * p.ldy + row;
       const float o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -537,7 +536,10 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
       // four layer rows, all loads before the first sum)
       int r0, n0;
       tile_of(p, pair_id, r0, n0);
-      const int live = min(p.bn, p.M - n0), row = r0 + 128 * int(rank) + 4 * lane;
+      // (no load is left in flight when the CTAs part: a CTA whose layer rows do not exist makes
+      // none, the others' results are stored by their first lanes at least)
+      const int row = r0 + 128 * int(rank) + 4 * lane;
+      const int live = r0 + 128 * int(rank) < p.R ? min(p.bn, p.M - n0) : 0;
       for (int t = split + splits * warp; t < live; t += splits * (THREADS / 32)) {
         const uint32_t at = tc::smem_u32(smem + (t * 128 + 4 * lane) * 4);
         float4 part[MAX_SPLITS];
@@ -633,10 +635,10 @@ int64_t clusters_at_once(int ctas, int sms) {
   return ctas <= 2 ? sms / ctas : ctas <= 4 ? sms * 2 / 9 : sms / 10;
 }
 
-cudaLaunchConfig_t cluster_launch(unsigned x, unsigned y, int cluster, int threads, int smem,
+cudaLaunchConfig_t cluster_launch(unsigned ctas, int cluster, int threads, int smem,
                                   cudaStream_t st, cudaLaunchAttribute (&at)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(x, y);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = st;
@@ -657,17 +659,15 @@ gptq_status launch_few(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, 
   if (!encode_codes(&wmap, wc, row_bytes, uint64_t(p.R), 128) ||
       !encode_codes(&xmap, xc, row_bytes, uint64_t(p.M), BN))
     return GPTQ_ERR_UNSUPPORTED;
-  const int rows = (p.R + 127) / 128, cols = (p.M + BN - 1) / BN;
+  const int rows = (p.R + 127) / 128;
   int splits = 1;
-  while (splits < 8 && int64_t(rows) * cols <= clusters_at_once(2 * splits, sms) &&
-         p.boxes >= 2 * C::SUB * splits)
+  while (splits < 8 && rows <= clusters_at_once(2 * splits, sms) && p.boxes >= 2 * C::SUB * splits)
     splits *= 2;
   GPTQ_CUDA(allow_smem(k_mx_few<BN, T>, C::SMEM));
   cudaLaunchAttribute at[2];
-  const cudaLaunchConfig_t cfg = cluster_launch(unsigned(rows * splits), unsigned(cols), splits,
-                                                FEW_THREADS, C::SMEM, st, at);
-  GPTQ_CUDA(cudaLaunchKernelEx(&cfg, k_mx_few<BN, T>, wmap, xmap, p, status));
-  note_launch();
+  const cudaLaunchConfig_t cfg = cluster_launch(unsigned(rows * splits), splits, FEW_THREADS,
+                                                C::SMEM, st, at);
+  GPTQ_LAUNCHED(cudaLaunchKernelEx(&cfg, k_mx_few<BN, T>, wmap, xmap, p, status), "k_mx_few");
   return GPTQ_OK;
 }
 
@@ -683,11 +683,10 @@ gptq_status launch_pair(cudaStream_t st, const uint32_t* xc, const uint32_t* wc,
   GPTQ_CUDA(allow_smem(pair::k_mx_pair<T>, pair::SMEM));
   const int clusters = int(std::min<int64_t>(sms / (2 * splits), int64_t(p.ntr) * p.ntt));
   cudaLaunchAttribute at[2];
-  const cudaLaunchConfig_t cfg = cluster_launch(unsigned(2 * splits * clusters), 1, 2 * splits,
+  const cudaLaunchConfig_t cfg = cluster_launch(unsigned(2 * splits * clusters), 2 * splits,
                                                 pair::THREADS, pair::SMEM, st, at);
-  GPTQ_CUDA(cudaLaunchKernelEx(&cfg, pair::k_mx_pair<T>, wmap, xmap, wsmap, xsmap, p,
-                               idesc_of(256, p.bn), status));
-  note_launch();
+  GPTQ_LAUNCHED(cudaLaunchKernelEx(&cfg, pair::k_mx_pair<T>, wmap, xmap, wsmap, xsmap, p,
+                                   idesc_of(256, p.bn), status), "k_mx_pair");
   return GPTQ_OK;
 }
 

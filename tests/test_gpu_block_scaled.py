@@ -156,7 +156,8 @@ SHAPES = [(1, 128, 64), (1, 1, 1), (2, 130, 32), (1, 513, 4128), (3, 100, 96), (
           # every width of a token tile, tiles that start in the middle of 128 tokens among them
           (256, 5120, 96), (384, 9472, 96), (500, 9472, 64), (700, 9472, 33),
           # few tiles and a long K, which several pairs share
-          (100, 300, 20000), (333, 513, 8200), (700, 130, 33000), (65, 2000, 1056), (129, 4000, 2100)]
+          (100, 300, 20000), (333, 513, 8200), (700, 130, 33000), (65, 2000, 1056), (129, 4000, 2100),
+          (70, 100, 9000), (70, 129, 9000)]
 
 
 @pytest.mark.parametrize("M,R,C", SHAPES)
