@@ -107,6 +107,24 @@ def test_quantize_edges():
     np.testing.assert_array_equal(np.nan_to_num(y, nan=0.0), np.nan_to_num(want, nan=0.0))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("order", ["near", "mixed"])
+def test_quantize_every_16_bit_value(dtype, order):
+    # every bit pattern once, in blocks of neighbours and in blocks of far-apart magnitudes
+    bits = np.arange(65536, dtype=np.uint16)
+    if order == "mixed":
+        bits = np.random.default_rng(0).permutation(bits)
+    t = torch.from_numpy(bits.view(np.int16)).view(dtype).reshape(-1, 32)
+    with np.errstate(invalid="ignore"):
+        c, e = L.mx_quantize(t.double().numpy())
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = MX.mx_quantize(t.to(DEV), st)
+    np.testing.assert_array_equal(q.codes.cpu().numpy().view(np.uint32), o.pack(c.astype(np.int64), 4))
+    got = q.scales.cpu().numpy().ravel()
+    np.testing.assert_array_equal(got[[L.mx_scale_index(r, 0, 1) for r in range(len(t))]], e[:, 0])
+    assert int(st) == G.GPTQ_ERR_NONFINITE
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_dequantize_every_code_and_scale(dtype):
     e = np.arange(256, dtype=np.uint8)[:, None]

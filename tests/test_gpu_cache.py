@@ -181,6 +181,51 @@ def test_values_at_the_edges(conf):
         np.testing.assert_array_equal(np.nan_to_num(got, nan=0.0), np.nan_to_num(vals, nan=0.0))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("conf", [CONFIGS[1], CONFIGS[2], CONFIGS[4], CONFIGS[7]], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("order", ["near", "mixed"])
+def test_every_16_bit_value(dtype, conf, order):
+    # every bit pattern once, in groups of neighbours and of far-apart magnitudes
+    bits = np.arange(65536, dtype=np.uint16)
+    if order == "mixed":
+        bits = np.random.default_rng(0).permutation(bits)
+    t = torch.from_numpy(bits.view(np.int16)).view(dtype).reshape(512, 1, 128)
+    with np.errstate(all="ignore"):
+        words, g, vals = _define(t.double().numpy(), *conf)
+    call = Call([512], [0], 64, 0)
+    pool = KV.KVCache.alloc(KV.make_cache_config(*conf), call.pages, 64, 1, 128)
+    pool.write(t.to(DEV), t.to(DEV), *call.args())
+    c = pool.k_codes.cpu().numpy().reshape(-1, 1, words.shape[-1])[call.slots]
+    np.testing.assert_array_equal(c.view(np.uint32), words)
+    K, V = pool.read(*call.args(), 512, torch.float32)
+    for got in (K.cpu().numpy(), V.cpu().numpy()):
+        np.testing.assert_array_equal(np.isnan(got), np.isnan(vals))
+        np.testing.assert_array_equal(np.nan_to_num(got, nan=0.0), np.nan_to_num(vals, nan=0.0))
+
+
+@pytest.mark.parametrize("power", [-95, -60, -1, 40, 88])
+@pytest.mark.parametrize("sym", [False, True])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_quotients_across_the_range_of_scales(bits, sym, power):
+    # ranges from below to above those that the kernel's products hold (2^-90 .. 2^90), among
+    # them ones whose width is a rounding away from a power of two
+    rng = np.random.default_rng([bits, power + 200])
+    x = (rng.standard_normal((300, 2, 64)) * 2.0 ** power).astype(np.float32)
+    x[:, 0] *= np.float32(1) + np.float32(2.0 ** -23)
+    x[::3] = np.rint(x[::3] / np.float32(2.0 ** (power - 4))) * np.float32(2.0 ** (power - 4))
+    conf = ("grid", bits, 32, sym)
+    with np.errstate(all="ignore"):
+        words, g, _ = _define(x.astype(np.float64), *conf)
+    call = Call([300], [0], 64, 0)
+    pool = KV.KVCache.alloc(KV.make_cache_config(*conf), call.pages, 64, 2, 64)
+    X = torch.from_numpy(x).to(DEV)
+    pool.write(X, X, *call.args())
+    c = pool.k_codes.cpu().numpy().reshape(-1, 2, words.shape[-1])[call.slots]
+    np.testing.assert_array_equal(c.view(np.uint32), words)
+    gr = pool.v_grids.cpu().numpy().reshape(-1, 2, 2, 2)[call.slots]
+    np.testing.assert_array_equal(gr, g)
+
+
 def test_rounding_near_ties_takes_the_exact_quotient():
     # values a few float32 steps around every half step of their group's 8-bit grid
     rng = np.random.default_rng(0)
