@@ -21,6 +21,7 @@
 // drains its own copies and MMAs before it frees TMEM and exits.
 #include <algorithm>
 
+#include "acc_ring.h"
 #include "kernels.h"
 #include "mx.cuh"
 #include "tc_common.cuh"
@@ -417,8 +418,8 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   } else if (warp == 1) {
     if (rank == 0) {
       int stage = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      int acc = 0;
+      uint32_t phase = 0;
+      AccRing ring(p.accs);
       bool ok = true;
       const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
       const uint64_t sdesc0 = tc::smem_desc_rows16(smem + s_off(p.bn));
@@ -430,8 +431,8 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         // a token tile may start in the middle of a scale tile, 32 tokens to a TMEM column; the
         // MMA takes its scales from an even column only, so tiles are multiples of 64 tokens
         const uint32_t first = uint32_t((n0 & 64) >> 5);
-        if (!wait(acc_empty + acc, acc_phase ^ 1u, true)) break;
-        const uint32_t d = tmem_base + uint32_t(acc * p.bn);
+        if (!wait(acc_empty + ring.at, ring.phase ^ 1u, true)) { ok = false; break; }
+        const uint32_t d = tmem_base + uint32_t(ring.at * p.bn);
         tc::fence_after_sync();
         for (int k = k0; k < k1; ++k) {
           if (!wait(full + stage, phase)) { ok = false; break; }
@@ -459,35 +460,39 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
                                   idesc | ((kk & 1) ? ODD_HALF : 0u), sfa + 4 * (kk >> 1),
                                   sfb + first + tile_cols * (kk >> 1), (k > k0 || kk > 0) ? 1u : 0u);
             tc::mma_commit_pair(empty + stage, both);
-            if (k + 1 == k1) tc::mma_commit_pair(acc_full + acc, both);
+            if (k + 1 == k1) tc::mma_commit_pair(acc_full + ring.at, both);
           }
           __syncwarp();
           if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
-        if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
+        ring.next();
       }
+      // every accumulator handed back: rank 1's last arrivals have landed in this CTA's shared
+      // memory before it can exit (they arrive before they store, so no store is waited for)
+      if (ok)
+        for (int i = 0; i < p.accs; ++i)
+          if (!wait(acc_empty + i, ring.last(i), true)) break;
     }
   } else {
     const int lane_base = (warp & 3) * 32;
     const int half = p.bn / 2, c0 = ((warp - 2) >> 2) * half;     // this warp's tokens of the tile
     const uint32_t acc_empty0 = tc::cluster_addr(acc_empty, base);
-    uint32_t acc_phase = 0;
-    int acc = 0;
+    AccRing ring(p.accs);
     for (int t = pair_id; t < tiles; t += n_pairs) {
       int r0, n0;
       tile_of(p, t, r0, n0);
-      if (!tc::mbar_wait_pair(acc_full + acc, acc_phase, abort_flag, peer_flag, p.wait_limit)) break;
+      if (!tc::mbar_wait_pair(acc_full + ring.at, ring.phase, abort_flag, peer_flag, p.wait_limit)) break;
       tc::fence_after_sync();
       uint32_t v[4][32];
-      const uint32_t at = tmem_base + (uint32_t(lane_base) << 16) + uint32_t(acc * p.bn + c0);
+      const uint32_t at = tmem_base + (uint32_t(lane_base) << 16) + uint32_t(ring.at * p.bn + c0);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (32 * c < half) tc::tmem_ld_32x32(at + 32 * c, v[c]);
       tc::tmem_ld_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster_relaxed(acc_empty0 + uint32_t(acc * 8));
-      if (++acc == p.accs) { acc = 0; acc_phase ^= 1u; }
+      if (lane == 0) tc::mbar_arrive_cluster_relaxed(acc_empty0 + uint32_t(ring.at * 8));
+      ring.next();
       const int row = r0 + 128 * int(rank) + lane_base + lane;
       if (splits > 1) {
         // this pair's partial sums, [token][128 rows]; every load into the ring was consumed

@@ -211,6 +211,20 @@ def test_product_of_small_whole_numbers_is_exact(M, R, C):
     np.testing.assert_array_equal(Y.cpu().numpy().astype(np.float64), x @ w.T)
 
 
+@pytest.mark.parametrize("M,R,C", [(700, 9572, 64), (256, 25601, 32), (130, 6273, 160)])
+def test_product_of_pairs_whose_second_half_has_no_rows(M, R, C):
+    # R % 256 in 1 .. 128: in the last row tile rank 1 of a pair only hands the accumulator back,
+    # and the pair parts at once; call upon call, each starting as the one before it drains
+    xc, xs, x = _stored(M, C, 1, 127, 128)
+    wc, ws, w = _stored(R, C, 2, 127, 128)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    Y = [torch.empty(M, R, device=DEV) for _ in range(4)]
+    for i in range(40):
+        MX.gptq_mx_matmul(xc, xs, wc, ws, C, Y[i % 4], st)
+    want = torch.from_numpy(x @ w.T).to(DEV)          # multiples of 1/4, far below 2^24 of them
+    assert int(st) == 0 and all(torch.equal(y.double(), want) for y in Y)
+
+
 @pytest.mark.parametrize("M", [1, 20, 200])
 def test_product_one_hot_reads_single_weights(M):
     # token t picks column t of W: any mistake in the order of columns, rows or scales shows

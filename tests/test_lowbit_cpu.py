@@ -265,6 +265,53 @@ def test_slot_arithmetic_on_the_host(tmp_path):
     assert out.tolist() == [(big - 1) * 2 ** 20 + 2 ** 20 - 2, (big - 1) * 2 ** 20 + 2 ** 20 - 1, -1]
 
 
+# ------------------------------------------------------------------ accumulators on the host
+def test_accumulators_are_all_handed_back_before_a_pair_parts(tmp_path):
+    # The device code's own turn-taking, compiled for the host, on a model of the barriers: the
+    # waits before each use pass as soon as the use before it was handed back and no sooner, and
+    # the waits at the end do not pass while any arrival of the last uses is outstanding.
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    src = tmp_path / "ring.cc"
+    src.write_text('#include "acc_ring.h"\n'
+                   "// passes of a barrier with `done` completed phases for a wait on `parity`\n"
+                   "static bool passes(int done, uint32_t parity) { return uint32_t(done & 1) != parity; }\n"
+                   'extern "C" int run(int accs, int tiles) {\n'
+                   "  gptq::AccRing mma(accs), epi(accs);\n"
+                   "  int uses[2] = {0, 0}, back[2] = {0, 0};\n"
+                   "  for (int t = 0; t < tiles; ++t) {\n"
+                   "    if (mma.at != t % accs) return 1;\n"
+                   "    // as late as it may be: handed back only when this use needs it\n"
+                   "    while (back[mma.at] < uses[mma.at]) {\n"
+                   "      if (passes(back[mma.at], mma.phase ^ 1u)) return 2;\n"
+                   "      if (epi.at != mma.at || epi.phase != (back[epi.at] & 1u)) return 3;\n"
+                   "      ++back[epi.at];\n"
+                   "      epi.next();\n"
+                   "    }\n"
+                   "    if (!passes(back[mma.at], mma.phase ^ 1u)) return 4;\n"
+                   "    ++uses[mma.at];\n"
+                   "    mma.next();\n"
+                   "  }\n"
+                   "  for (int i = 0; i < accs; ++i) {\n"
+                   "    if (uses[i] - back[i] > 1) return 5;\n"
+                   "    if (back[i] < uses[i] && passes(back[i], mma.last(i))) return 6;   // outstanding\n"
+                   "    if (!passes(uses[i], mma.last(i))) return 7;                       // landed, or never used\n"
+                   "  }\n"
+                   "  return 0; }\n")
+    so = tmp_path / "ring.so"
+    subprocess.run([cxx, "-O1", "-shared", "-fPIC", "-I",
+                    os.path.join(ROOT, "post_weight_quantization_20_b200", "csrc"), str(src), "-o",
+                    str(so)], check=True)
+    run = ctypes.CDLL(str(so)).run
+    for accs in (1, 2):
+        for tiles in range(12):
+            assert run(accs, tiles) == 0, (accs, tiles)
+    # and the product's MMA warp makes those waits
+    src = open(os.path.join(ROOT, "post_weight_quantization_20_b200", "csrc", "mx_matmul.cu")).read()
+    assert "wait(acc_empty + i, ring.last(i), true)" in src
+
+
 # ------------------------------------------------------------------ the definitions
 def test_mx_definition_on_hand_worked_blocks():
     x = np.zeros((4, 32))
