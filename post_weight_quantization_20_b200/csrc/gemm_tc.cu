@@ -207,7 +207,7 @@ k_gemm3_tf32(const __grid_constant__ CUtensorMap ahi, const __grid_constant__ CU
 #pragma unroll
       for (int q = 0; q < 128; ++q) r[q] = 0.f;
       for (int s = 0; s < p.nk; ++s) {
-        if (!tc::mbar_wait(acc_full + acc, acc_phase, abort_flag, p.wait_limit)) { ok = false; break; }
+        if (!tc::mbar_wait_warp(acc_full + acc, acc_phase, abort_flag, p.wait_limit)) { ok = false; break; }
         tc::fence_after_sync();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {

@@ -221,7 +221,7 @@ k_hess_syrk_tc(const __grid_constant__ CUtensorMap xmap, float* H, Sched s, floa
 #pragma unroll
       for (int q = 0; q < 128; ++q) r[q] = 0.f;
       for (int ks = k0; ks < k1; ks += SEG) {
-        if (!tc::mbar_wait(acc_full + acc, acc_phase, abort_flag, s.wait_limit)) { ok = false; break; }
+        if (!tc::mbar_wait_warp(acc_full + acc, acc_phase, abort_flag, s.wait_limit)) { ok = false; break; }
         tc::fence_after_sync();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -473,7 +473,7 @@ k_hess_syrk_pair(const __grid_constant__ CUtensorMap xmap, float* H, Sched s, fl
 #pragma unroll
       for (int q = 0; q < 128; ++q) r[q] = 0.f;
       for (int ks = k0; ks < k1; ks += SEG) {
-        if (!tc::mbar_wait_pair(acc_full + acc, acc_phase, abort_flag, peer_flag, s.wait_limit)) { ok = false; break; }
+        if (!tc::mbar_wait_pair_warp(acc_full + acc, acc_phase, abort_flag, peer_flag, s.wait_limit)) { ok = false; break; }
         tc::fence_after_sync();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {

@@ -128,8 +128,7 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
     int stage = 0;
     uint32_t phase = 0;
     for (int b = b0; b < b1; b += C::SUB) {
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(empty + stage, phase ^ 1u, abort_flag, p.wait_limit)))
-        break;
+      if (!tc::mbar_wait_warp(empty + stage, phase ^ 1u, abort_flag, p.wait_limit)) break;
       const int nbx = min(C::SUB, b1 - b);
       uint8_t* a = smem + stage * C::STAGE;
       uint8_t* x = a + C::SUB * A_BOX;
@@ -156,7 +155,7 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
     const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
     const uint64_t sdesc0 = tc::smem_desc_rows16(smem + C::SUB * (A_BOX + C::B_BOX));
     for (int b = b0; b < b1; b += C::SUB) {
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(full + stage, phase, abort_flag, p.wait_limit));
+      ok = tc::mbar_wait_warp(full + stage, phase, abort_flag, p.wait_limit);
       if (!ok) break;
       tc::fence_after_sync();
       // descriptors count in 16 bytes
@@ -191,7 +190,7 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
     // lane base + lane is a layer row, a TMEM column a token
     const int lane_base = (warp & 3) * 32;
     const int row = r0 + lane_base + lane;
-    if (tc::mbar_wait(acc_full, 0, abort_flag, p.wait_limit)) {
+    if (tc::mbar_wait_warp(acc_full, 0, abort_flag, p.wait_limit)) {
       tc::fence_after_sync();
       float* part = reinterpret_cast<float*>(smem);      // [token][128 rows]; the ring is empty
       for (int c = 0; c < p.M; c += 16) {
@@ -387,8 +386,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     tc::tma_load_2d_pair(s + SUB * 1024, &xsmap, k * 256, n0 / 128, cbar);
   };
   const auto wait = [&](uint64_t* bar, uint32_t parity, bool cluster_scope = false) {
-    return __all_sync(0xffffffffu, tc::mbar_wait_pair(bar, parity, abort_flag, peer_flag, p.wait_limit,
-                                                      cluster_scope));
+    return tc::mbar_wait_pair_warp(bar, parity, abort_flag, peer_flag, p.wait_limit, cluster_scope);
   };
 
   allow_successor();
@@ -481,7 +479,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     for (int t = pair_id; t < tiles; t += n_pairs) {
       int r0, n0;
       tile_of(p, t, r0, n0);
-      if (!tc::mbar_wait_pair(acc_full + ring.at, ring.phase, abort_flag, peer_flag, p.wait_limit)) break;
+      if (!wait(acc_full + ring.at, ring.phase)) break;
       tc::fence_after_sync();
       uint32_t v[4][32];
       const uint32_t at = tmem_base + (uint32_t(lane_base) << 16) + uint32_t(ring.at * p.bn + c0);

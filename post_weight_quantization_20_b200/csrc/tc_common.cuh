@@ -72,6 +72,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return false;
 }
 
+// The same by a whole warp, whose lanes go on together and with one answer: each counts its own
+// polls, and where a wait gives up some may see the phase complete and others not.  The .aligned
+// instructions that follow (tcgen05.ld, tcgen05.wait) need every lane of the warp or none.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               uint32_t limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit));
+}
+
 // Bounded wait that does not stop at the abort flag.  After an abort, the thread
 // that issued TMA copies or MMAs waits with it until they have landed, so that
 // the CTA frees TMEM and exits with none of its own copies in flight.
@@ -349,6 +357,13 @@ __device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, v
   st_cluster_u32(peer_flag, 1u);
   asm volatile("fence.acq_rel.cluster;" ::: "memory");   // before any later cluster barrier
   return false;
+}
+
+// The same by a whole warp (see mbar_wait_warp).
+__device__ __forceinline__ bool mbar_wait_pair_warp(uint64_t* bar, uint32_t parity,
+                                                    volatile int* abort_flag, uint32_t peer_flag,
+                                                    uint32_t limit, bool cluster_scope = false) {
+  return __all_sync(0xffffffffu, mbar_wait_pair(bar, parity, abort_flag, peer_flag, limit, cluster_scope));
 }
 
 // 2-D TMA load into this CTA's shared memory whose completion is counted on an

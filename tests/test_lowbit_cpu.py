@@ -312,6 +312,20 @@ def test_accumulators_are_all_handed_back_before_a_pair_parts(tmp_path):
     assert "wait(acc_empty + i, ring.last(i), true)" in src
 
 
+def test_epilogues_wait_as_whole_warps():
+    # tcgen05.ld is .aligned: the wait before it must give all lanes of a warp one answer
+    csrc = os.path.join(ROOT, "post_weight_quantization_20_b200", "csrc")
+    votes = {"mbar_wait_warp", "mbar_wait_pair_warp", "wait"}
+    found = 0
+    for name in ("mx_matmul.cu", "gemm_tc.cu", "hessian_tc.cu"):
+        src = open(os.path.join(csrc, name)).read()
+        calls = set(re.findall(r"(\w*wait\w*)\(acc_full\b", src))
+        assert calls and calls <= votes, (name, calls)
+        found += len(re.findall(r"wait\w*\(acc_full\b", src))
+    assert found == 5
+    assert "return tc::mbar_wait_pair_warp(bar," in open(os.path.join(csrc, "mx_matmul.cu")).read()
+
+
 # ------------------------------------------------------------------ the definitions
 def test_mx_definition_on_hand_worked_blocks():
     x = np.zeros((4, 32))
