@@ -516,12 +516,13 @@ k_hess_syrk_pair(const __grid_constant__ CUtensorMap xmap, float* H, Sched s, fl
   tc::cluster_sync();          // both CTAs out of their loops: the abort flags are final
   if (*abort_flag) {
     // A wait gave up in one of the CTAs, which raised both flags.  (1) rank 0's MMAs
-    // land; (2) the producers exchange their fill counts and the one behind fills
-    // the phases the other filled (a box at the origin), so every phase of rank 0's
-    // full barriers that either CTA loaded into completes; (3) rank 0 waits for
-    // them, i.e. for both CTAs' copies; (4) neither CTA exits before that.
-    if (warp == 1 && lane == 0 && rank == 0) {
-      tc::mma_commit_pair(drain, 0x1);
+    // land, and in both CTAs the arrival behind all those that they made there; (2) the
+    // producers exchange their fill counts and the one behind fills the phases the other
+    // filled (a box at the origin), so every phase of rank 0's full barriers that either
+    // CTA loaded into completes; (3) rank 0 waits for them, i.e. for both CTAs' copies;
+    // (4) neither CTA exits before that.
+    if (warp == 1 && lane == 0) {
+      if (rank == 0) tc::mma_commit_pair(drain, 0x3);
       tc::mbar_drain(drain, 0);
     }
     if (warp == 0 && lane == 0)

@@ -569,14 +569,15 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
   }
   tc::cluster_sync_relaxed();  // all CTAs out of their loops: the abort flags are final
   if (*abort_flag) {
-    // A wait gave up in one of the CTAs, which raised both flags.  (1) rank 0's MMAs land;
-    // (2) the producers exchange their fill counts and the one behind fills the phases the
-    // other filled (boxes at the origin), so every phase of rank 0's full barriers that either
-    // CTA loaded into completes; (3) rank 0 waits for them, i.e. for both CTAs' copies;
-    // (4) neither CTA exits before that.
-    if (warp == 1 && rank == 0) {    // by the lane that issued the MMAs
+    // A wait gave up in one of the CTAs, which raised both flags.  (1) rank 0's MMAs land, and
+    // in both CTAs the arrival behind all those that they made there; (2) the producers
+    // exchange their fill counts and the one behind fills the phases the other filled (boxes at
+    // the origin), so every phase of rank 0's full barriers that either CTA loaded into
+    // completes; (3) rank 0 waits for them, i.e. for both CTAs' copies; (4) neither CTA exits
+    // before that.
+    if (warp == 1) {
       if (tc::elect_one()) {
-        tc::mma_commit_pair(drain, uint16_t(1u << base));
+        if (rank == 0) tc::mma_commit_pair(drain, both);    // by the lane that issued the MMAs
         tc::mbar_drain(drain, 0);
       }
       __syncwarp();

@@ -326,6 +326,14 @@ def test_epilogues_wait_as_whole_warps():
     assert "return tc::mbar_wait_pair_warp(bar," in open(os.path.join(csrc, "mx_matmul.cu")).read()
 
 
+def test_both_ctas_of_a_pair_see_the_end_of_an_abort():
+    # the issuer's arrivals reach both CTAs of a pair; after a wait gave up, both wait for the last
+    csrc = os.path.join(ROOT, "post_weight_quantization_20_b200", "csrc")
+    for name, both in (("mx_matmul.cu", "both"), ("hessian_tc.cu", "0x3")):
+        src = open(os.path.join(csrc, name)).read()
+        assert set(re.findall(r"mma_commit_pair\([^,]+, ([^)]+)\)", src)) == {both}, name
+
+
 # ------------------------------------------------------------------ the definitions
 def test_mx_definition_on_hand_worked_blocks():
     x = np.zeros((4, 32))
