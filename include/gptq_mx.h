@@ -74,6 +74,17 @@ gptq_status gptq_mx_matmul(const uint32_t* x_codes, const uint8_t* x_scales, int
                            int64_t cols, void* Y, int ydtype, int64_t ldy, int32_t* dev_status,
                            void* stream);
 
+/*
+ * Diagnostic: in products launched after this call the MMA issuer of the last CTA (or CTA pair)
+ * of every cluster gives up when it comes to its stage number `stages` of a tile, with the
+ * copies and MMAs of the stages before it in flight; -1, the default, restores normal work.
+ * The call then reports TIMEOUT and its Y is not defined, as where a wait runs out
+ * (gptq_debug_set_wait_limit), but at a known place: so a test can check that CTAs which share
+ * a tile's columns stop together, wait for what they have in flight and leave the context
+ * usable.  Process-wide; returns the previous value.
+ */
+int32_t gptq_mx_debug_give_up(int32_t stages);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,4 +1,5 @@
 // The C ABI of the microscaled 4-bit rows (include/gptq_mx.h): argument checks and dispatch.
+#include <atomic>
 #include <climits>
 
 #include "gptq_mx.h"
@@ -12,7 +13,16 @@ static bool valid_shape(int64_t rows, int64_t cols) {
   return rows >= 0 && rows <= INT_MAX && cols > 0 && cols <= INT_MAX / 2;
 }
 
+static std::atomic<int32_t> g_give_up{-1};
+namespace gptq {
+int mx_give_up() { return g_give_up.load(std::memory_order_relaxed); }
+}  // namespace gptq
+
 extern "C" {
+
+int32_t gptq_mx_debug_give_up(int32_t stages) {
+  return g_give_up.exchange(stages < 0 ? -1 : stages, std::memory_order_relaxed);
+}
 
 size_t gptq_mx_scale_bytes(int64_t rows, int64_t cols) {
   if (!valid_shape(rows, cols)) return 0;

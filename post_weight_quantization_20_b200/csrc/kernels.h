@@ -73,6 +73,8 @@ gptq_status mx_dequantize_run(cudaStream_t st, const uint32_t* codes, const uint
 gptq_status mx_matmul_run(cudaStream_t st, const uint32_t* xc, const uint8_t* xs, int M,
                           const uint32_t* wc, const uint8_t* ws, int R, int C, void* Y, int dt,
                           int64_t ldy, int32_t* status);
+// abi_mx.cu: the stage at which its last MMA issuer gives up (-1: none)
+int mx_give_up();
 
 // kv_cache.cu: words of codes and groups of one token and head (false: not supported), and
 // the two passes over the rows of a call (write: into the cache)

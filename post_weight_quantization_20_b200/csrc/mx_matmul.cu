@@ -42,6 +42,7 @@ struct Prob {
   int ct;            // scale tiles along K: 128 columns each
   int boxes;         // boxes along K: 256 columns each
   uint32_t wait_limit;
+  int give_up;       // stage of a tile at which the last MMA issuer gives up (-1: none)
   // k_mx_pair only
   int bn;            // tokens of a tile, a multiple of 64
   int nb;            // scale tiles that a token tile touches
@@ -152,10 +153,11 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
     uint32_t phase = 0;
     bool ok = true;
     constexpr uint32_t idesc = idesc_of(128, BN);
+    const int last = p.give_up >= 0 && split == splits - 1 ? b0 + C::SUB * p.give_up : b1;
     const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
     const uint64_t sdesc0 = tc::smem_desc_rows16(smem + C::SUB * (A_BOX + C::B_BOX));
     for (int b = b0; b < b1; b += C::SUB) {
-      ok = tc::mbar_wait_warp(full + stage, phase, abort_flag, p.wait_limit);
+      ok = tc::mbar_wait_warp(full + stage, phase, abort_flag, b < last ? p.wait_limit : 0u);
       if (!ok) break;
       tc::fence_after_sync();
       // descriptors count in 16 bytes
@@ -385,8 +387,9 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
     tc::tma_load_2d_pair(s, &wsmap, k * 256, r0 / 128 + int(rank), cbar);
     tc::tma_load_2d_pair(s + SUB * 1024, &xsmap, k * 256, n0 / 128, cbar);
   };
-  const auto wait = [&](uint64_t* bar, uint32_t parity, bool cluster_scope = false) {
-    return tc::mbar_wait_pair_warp(bar, parity, abort_flag, peer_flag, p.wait_limit, cluster_scope);
+  const auto wait = [&](uint64_t* bar, uint32_t parity, bool cluster_scope = false, bool give_up = false) {
+    return tc::mbar_wait_pair_warp(bar, parity, abort_flag, peer_flag, give_up ? 0u : p.wait_limit,
+                                   cluster_scope);
   };
 
   allow_successor();
@@ -421,6 +424,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
       bool ok = true;
       const uint64_t adesc0 = tc::smem_desc_sw128(smem, 16, 1024);
       const uint64_t sdesc0 = tc::smem_desc_rows16(smem + s_off(p.bn));
+      const int last = p.give_up >= 0 && split == splits - 1 ? k0 + p.give_up : k1;
       const uint32_t xbox = uint32_t(p.bn / 2 * KB) >> 4;       // descriptors count in 16 bytes
       const uint32_t tile_cols = 4 * uint32_t(p.nb);            // TMEM columns of 128 columns' scales of X
       for (int t = pair_id; t < tiles && ok; t += n_pairs) {
@@ -433,7 +437,7 @@ k_mx_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUte
         const uint32_t d = tmem_base + uint32_t(ring.at * p.bn);
         tc::fence_after_sync();
         for (int k = k0; k < k1; ++k) {
-          if (!wait(full + stage, phase)) { ok = false; break; }
+          if (!wait(full + stage, phase, false, k >= last)) { ok = false; break; }
           tc::fence_after_sync();
           const uint64_t ad = adesc0 + uint32_t(stage * (bytes >> 4));
           const uint64_t xd = ad + (x_off() >> 4);
@@ -747,6 +751,7 @@ gptq_status mx_matmul_run(cudaStream_t st, const uint32_t* xc, const uint8_t* xs
   p.ct = (nb + 3) / 4;
   p.boxes = (nb + 7) / 8;
   p.wait_limit = pipeline_wait_limit();
+  p.give_up = int(std::min<int64_t>(mx_give_up(), p.boxes));
   const uint64_t row_bytes = uint64_t(nb) * 16;
   switch (dt) {
     case GPTQ_F32: return by_tokens<float>(st, xc, wc, row_bytes, p, sms, status);

@@ -20,7 +20,8 @@ import torch
 from . import gptq as G
 
 # every symbol include/gptq_mx.h declares
-EXPORTS = ("gptq_mx_scale_bytes", "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_matmul")
+EXPORTS = ("gptq_mx_scale_bytes", "gptq_mx_quantize", "gptq_mx_dequantize", "gptq_mx_matmul",
+           "gptq_mx_debug_give_up")
 
 _lib = None
 
@@ -39,6 +40,8 @@ def load_library() -> ctypes.CDLL:
         lib.gptq_mx_dequantize.restype = i32
         lib.gptq_mx_matmul.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i32, i64, vp, vp]
         lib.gptq_mx_matmul.restype = i32
+        lib.gptq_mx_debug_give_up.argtypes = [ctypes.c_int32]
+        lib.gptq_mx_debug_give_up.restype = ctypes.c_int32
         _lib = lib
     return _lib
 
@@ -142,6 +145,12 @@ def gptq_mx_matmul(x_codes, x_scales, w_codes, w_scales, cols, Y, status=None,
     _call(load_library().gptq_mx_matmul, "gptq_mx_matmul", dev, stream, x_codes.data_ptr(),
           x_scales.data_ptr(), M, w_codes.data_ptr(), w_scales.data_ptr(), R, cols, Y.data_ptr(),
           dt, ld, st)
+
+
+def gptq_mx_debug_give_up(stages: int) -> int:
+    """Stage of a tile at which the products' last MMA issuer gives up (-1: none); returns the
+    previous one.  For tests of the timeout path."""
+    return int(load_library().gptq_mx_debug_give_up(int(stages)))
 
 
 # --------------------------------------------------------------------------- whole matrices

@@ -382,3 +382,33 @@ def test_product_waits_give_up_and_drain(M, R, C, shared):
     rows = slice(0, 300)
     np.testing.assert_array_equal(Y[:, rows].double().cpu().numpy(), x @ w[rows].T)
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("M,R,C,stage", [
+    # one CTA a tile; K split over eight CTAs of a cluster
+    (4, 9600, 4096, 0), (4, 9600, 4096, 6), (16, 300, 49152, 0), (16, 300, 49152, 3), (16, 300, 49152, 11),
+    (60, 300, 20000, 2),
+    # a pair a tile, of several tiles each; pairs that share a tile's K
+    (512, 9500, 2080, 0), (512, 9500, 2080, 4), (2000, 2000, 5120, 7),
+    (300, 1000, 49152, 0), (300, 1000, 49152, 5), (300, 1000, 49152, 20), (65, 200, 9000, 1)])
+def test_product_that_gives_up_at_a_stage_stops_as_one(M, R, C, stage):
+    # the last CTA or pair of each cluster stops in the middle of its work: the status says so every
+    # time, and the same calls then compute the right values
+    xc, xs, x = _stored(M, C, 1, 127, 128)
+    wc, ws, w = _stored(R, C, 2, 127, 128)
+    Y = torch.empty(M, R, device=DEV)
+    st = torch.zeros(3, dtype=torch.int32, device=DEV)
+    assert MX.gptq_mx_debug_give_up(stage) == -1
+    try:
+        for i in range(3):
+            MX.gptq_mx_matmul(xc, xs, wc, ws, C, Y, st[i:i + 1])
+        torch.cuda.synchronize()
+    finally:
+        assert MX.gptq_mx_debug_give_up(-1) == stage
+    assert st.tolist() == [G.GPTQ_ERR_TIMEOUT] * 3
+    st.zero_()
+    Y.fill_(float("nan"))
+    MX.gptq_mx_matmul(xc, xs, wc, ws, C, Y, st[:1])
+    rows = slice(0, 300)                              # multiples of 1/4, sums below 2^24 of them
+    np.testing.assert_array_equal(Y[:, rows].double().cpu().numpy(), x @ w[rows].T)
+    assert int(st[0]) == 0 and not Y.isnan().any()

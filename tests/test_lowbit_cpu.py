@@ -107,6 +107,12 @@ def test_mx_matmul_refuses_bad_arguments():
         assert call(**over) == OK, over
 
 
+def test_give_up_stage_is_off_by_default_and_returned():
+    assert MX.gptq_mx_debug_give_up(3) == -1
+    assert MX.gptq_mx_debug_give_up(-7) == 3
+    assert MX.gptq_mx_debug_give_up(-1) == -1
+
+
 def _cache_args(cfg=None, **over):
     c = dict(k_codes=4096, k_grids=4096, v_codes=4096, v_grids=4096, pages=4, page_size=16,
              heads=2, dim=64)
