@@ -65,7 +65,8 @@ gptq_status gptq_mx_dequantize(const uint32_t* codes, const uint8_t* scales, int
  * rows x cols (w_codes, w_scales), Y m_tokens x rows with row stride ldy elements, ydtype.
  *     Y[t][r] = sum_c x[t][c] w[r][c]
  * Products are exact, sums are held in fp32 and rounded once to ydtype.  Any m_tokens, rows
- * >= 0 (0: a no-op) and cols >= 1; one token is as good a case as many.  A block of either
+ * from 0 (a no-op) to 2^31 - 256, not more than 2^30 tiles of 64 x 256 in all, and cols >= 1;
+ * one token is as good a case as many.  A block of either
  * side with e = 255 makes the outputs of its row NaN.  Device conditions: TIMEOUT.
  * Errors: INVALID_ARG, UNSUPPORTED (the driver cannot encode the operands' tensor maps).
  */

@@ -12,6 +12,12 @@ static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 static bool valid_shape(int64_t rows, int64_t cols) {
   return rows >= 0 && rows <= INT_MAX && cols > 0 && cols <= INT_MAX / 2;
 }
+// Rows and tokens of a product: indices of rows in a last tile of 256, and the number of tiles
+// (256 rows x 64 tokens at the least), are ints.
+static bool valid_product(int64_t rows, int64_t tokens) {
+  return rows <= INT_MAX - 255 && tokens <= INT_MAX - 255 &&
+         (rows + 255) / 256 * ((tokens + 63) / 64) <= int64_t(1) << 30;
+}
 
 static std::atomic<int32_t> g_give_up{-1};
 namespace gptq {
@@ -57,8 +63,8 @@ gptq_status gptq_mx_matmul(const uint32_t* x_codes, const uint8_t* x_scales, int
                            int64_t cols, void* Y, int ydtype, int64_t ldy, int32_t* dev_status,
                            void* stream) {
   CallRange range_("gptq_mx_matmul");
-  if (!valid_shape(rows, cols) || !valid_shape(m_tokens, cols) || !valid_dtype(ydtype) ||
-      ldy < rows)
+  if (!valid_shape(rows, cols) || !valid_shape(m_tokens, cols) || !valid_product(rows, m_tokens) ||
+      !valid_dtype(ydtype) || ldy < rows)
     return GPTQ_ERR_INVALID_ARG;
   if (rows == 0 || m_tokens == 0) return GPTQ_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !Y || !aligned16(x_codes) ||

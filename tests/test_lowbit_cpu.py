@@ -107,6 +107,21 @@ def test_mx_matmul_refuses_bad_arguments():
         assert call(**over) == OK, over
 
 
+@no_gpu
+def test_mx_matmul_refuses_sizes_past_its_index_arithmetic():
+    f, top = MX.load_library().gptq_mx_matmul, 2 ** 31 - 1
+    launched = (G.GPTQ_ERR_CUDA,)                        # past the checks: there is no GPU here
+
+    def call(M, R):
+        return f(FAKE, FAKE, M, FAKE, FAKE, R, 32, FAKE, 0, R, None, None)
+
+    for M, R in ((1, top), (top, 1), (1, top - 254), (top - 254, 1), (100, top - 100),
+                 (2 ** 23, 2 ** 22 * 8), (top - 255, top - 255)):
+        assert call(M, R) == INVALID, (M, R)
+    for M, R in ((1, top - 255), (top - 255, 1), (2 ** 22, 2 ** 22)):
+        assert call(M, R) in launched, (M, R)
+
+
 def test_give_up_stage_is_off_by_default_and_returned():
     assert MX.gptq_mx_debug_give_up(3) == -1
     assert MX.gptq_mx_debug_give_up(-7) == 3
