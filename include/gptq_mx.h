@@ -64,7 +64,10 @@ gptq_status gptq_mx_dequantize(const uint32_t* codes, const uint8_t* scales, int
  * gptq_mx_matmul — Y = X W^T of two stored forms: X m_tokens x cols (x_codes, x_scales), W
  * rows x cols (w_codes, w_scales), Y m_tokens x rows with row stride ldy elements, ydtype.
  *     Y[t][r] = sum_c x[t][c] w[r][c]
- * Products are exact, sums are held in fp32 and rounded once to ydtype.  Any m_tokens, rows
+ * Products are exact, sums are held in fp32 and rounded once to ydtype.  Scales reach further
+ * than fp32 does, from 2^-254 to 2^254 for a pair of blocks: what of a product or a sum lies
+ * below 2^-149, fp32's least subnormal, is cut off; a sum beyond fp32's range is an infinity,
+ * and NaN once infinities of both signs have met.  Any m_tokens, rows
  * from 0 (a no-op) to 2^31 - 256, not more than 2^30 tiles of 64 x 256 in all, and cols >= 1;
  * one token is as good a case as many.  A block of either
  * side with e = 255 makes the outputs of its row NaN.  Device conditions: TIMEOUT.

@@ -211,6 +211,52 @@ def test_product_of_small_whole_numbers_is_exact(M, R, C):
     np.testing.assert_array_equal(Y.cpu().numpy().astype(np.float64), x @ w.T)
 
 
+@pytest.mark.parametrize("M,R,C", [(5, 300, 4128), (16, 130, 9000), (130, 300, 700), (100, 300, 9000)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("ex,ew", [((0, 30), (85, 125)), ((60, 100), (0, 30)), ((225, 255), (80, 109)),
+                                   ((0, 2), (253, 255)), ((253, 255), (0, 2))])
+def test_product_at_the_ends_of_the_scales(M, R, C, dtype, ex, ew):
+    # the bound of test_product_within_its_bound where products and sums lie about fp32's least or
+    # below its largest number: each of the cuts counted there is at least one of 2^-149, and the
+    # last rounding at least half of the type's least subnormal
+    xc, xs, x = _stored(M, C, 1, *ex)
+    wc, ws, w = _stored(R, C, 2, *ew)
+    Y = torch.empty(M, R, dtype=dtype, device=DEV)
+    MX.gptq_mx_matmul(xc, xs, wc, ws, C, Y)
+    got, want, S = Y.double().cpu().numpy(), x @ w.T, np.abs(x) @ np.abs(w).T
+    assert S.max() < 2.0 ** 127                            # no sum overflows
+    f = torch.finfo(dtype)
+    bound = (2 * -(-C // 64) + 16) * (2.0 ** -23 * S + 2.0 ** -149)
+    bound = bound + f.eps / 2 * (np.abs(want) + bound) + f.smallest_normal * f.eps / 2
+    if dtype == torch.float16:
+        edge = 65520.0                                     # what rounds to 65504 or less in magnitude
+        inf = np.abs(want) - bound >= edge
+        assert np.array_equal(np.isinf(got) & inf, inf)
+        near = ~inf & (np.abs(want) + bound >= edge)       # either
+        got = np.where(inf | near, 0, got)
+        want = np.where(inf | near, 0, want)
+    assert np.all(np.abs(got - want) <= bound)
+
+
+@pytest.mark.parametrize("M", [3, 100])
+def test_product_past_the_range_is_infinite(M):
+    # sums of one sign: beyond fp32's range an infinity of that sign, whatever their order
+    R, C = 140, 1000
+    rng = np.random.default_rng(0)
+    cx, cw = (rng.integers(1, 8, (n, 1024)).astype(np.uint8) for n in (M, R))
+    cw[1::2] |= 8
+    cx[:, C:], cw[:, C:] = 0, 0
+    ex, ew = np.full((M, 32), 254, np.uint8), np.full((R, 32), 254, np.uint8)
+    ex[1] = 0                                              # 2^-127 x 2^127: an ordinary sum
+    Y = torch.empty(M, R, device=DEV)
+    MX.gptq_mx_matmul(*_device(cx, ex, C), *_device(cw, ew, C), C, Y)
+    y, want = Y.double().cpu().numpy(), L.mx_values(cx, ex)[:, :C] @ L.mx_values(cw, ew)[:, :C].T
+    np.testing.assert_array_equal(y[1], want[1])           # multiples of 1/4, below 2^24 of them
+    rest = np.arange(M) != 1
+    assert np.all(np.abs(want[rest]) > 2.0 ** 128)
+    np.testing.assert_array_equal(y[rest], np.where(want[rest] > 0, np.inf, -np.inf))
+
+
 @pytest.mark.parametrize("M,R,C", [(700, 9572, 64), (256, 25601, 32), (130, 6273, 160)])
 def test_product_of_pairs_whose_second_half_has_no_rows(M, R, C):
     # R % 256 in 1 .. 128: in the last row tile rank 1 of a pair only hands the accumulator back,
