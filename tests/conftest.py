@@ -22,6 +22,9 @@ def _has_cuda():
 
 
 def pytest_collection_modifyitems(config, items):
+    # the full-size cases last (the order is otherwise kept): a run that is cut short has then
+    # been through every other test
+    items.sort(key=lambda it: "slow" in it.keywords)
     if _has_cuda():
         return
     skip = pytest.mark.skip(reason="no CUDA device")
