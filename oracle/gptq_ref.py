@@ -59,6 +59,8 @@ fixtures, brute force and independent solves in ``tests/test_oracle_pins.py``.
 """
 from __future__ import annotations
 
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import scipy.linalg as sla
 
@@ -70,16 +72,40 @@ class NotPositiveDefinite(ArithmeticError):
 # -----------------------------------------------------------------------------
 # step 1: Hessian  [Deep-dive §3.1 step 1], [Deep-dive §2.1]
 # -----------------------------------------------------------------------------
+XTX_MAX = 8192      # columns whose X^T X is one product
+XTX_BLOCK = 2048    # columns of a block of a wider one
+
+
+def _blocks(n: int, size: int = XTX_BLOCK):
+    return [slice(k, min(k + size, n)) for k in range(0, n, size)]
+
+
+def _in_threads(f, items) -> None:
+    """f of each item; the copies and updates of wide matrices keep one core busy each."""
+    with ThreadPoolExecutor() as pool:
+        list(pool.map(f, items))
+
+
+def _mirror(G: np.ndarray) -> None:
+    """The blocks above the diagonal from those below it."""
+    def rows(j):
+        for i in _blocks(j.start):
+            G[i, j] = G[j, i].T
+
+    _in_threads(rows, _blocks(len(G)))
+
+
 def _xtx(Xd: np.ndarray) -> np.ndarray:
-    """X^T X by general matrix products over blocks of at most 8192 columns (the
-    symmetric rank-k routine behind a plain X.T @ X fails in OpenBLAS once the
-    result has 2^31 or more entries, e.g. 49152 x 49152)."""
+    """X^T X; a wide one by block columns (the symmetric rank-k routine behind a plain
+    X.T @ X fails in OpenBLAS once the result has 2^31 or more entries, e.g. 49152 x
+    49152), each from its diagonal block down, and their mirror images."""
     C = Xd.shape[1]
-    if C <= 8192:
+    if C <= XTX_MAX:
         return Xd.T @ Xd
     G = np.empty((C, C))
-    for j0 in range(0, C, 8192):
-        G[:, j0:j0 + 8192] = Xd.T @ Xd[:, j0:j0 + 8192]
+    for j in _blocks(C):
+        np.matmul(Xd[:, j.start:].T, Xd[:, j], out=G[j.start:, j])
+    _mirror(G)
     return G
 
 
@@ -92,28 +118,41 @@ def hessian_accumulate(H: np.ndarray, n: int, X: np.ndarray):
     if m == 0:
         return H, n
     Xd = np.asarray(X, dtype=np.float64)
-    H = H * (n / (n + m)) + (2.0 / (n + m)) * _xtx(Xd)
-    return H, n + m
+    G = _xtx(Xd)
+    G *= 2.0 / (n + m)
+    G += H * (n / (n + m))
+    return G, n + m
 
 
 def hessian(X: np.ndarray, chunk: int | None = None):
     """H = 2/n X^T X over all tokens of X, accumulated chunk by chunk with the same
-    running-mean update as hessian_accumulate (each entry rounded the same way; the
-    update is done in place on H so that a wide layer needs no C x C temporaries
-    beyond the chunk's X^T X)."""
+    running-mean update as hessian_accumulate (each entry rounded the same way).  A wide
+    layer's H is updated in place by block columns, each from its diagonal block down, and
+    mirrored once: it needs no C x C temporaries, and half the products."""
     cols = X.shape[1]
     H = np.zeros((cols, cols))
     n = 0
     step = chunk or max(1, X.shape[0])
+    wide = cols > XTX_MAX
+    G = np.empty((cols, XTX_BLOCK)) if wide else None
     for t in range(0, X.shape[0], step):
         Xd = np.asarray(X[t:t + step], dtype=np.float64)
         m = int(Xd.shape[0])
-        G = _xtx(Xd)
-        G *= 2.0 / (n + m)
-        H *= n / (n + m)
-        H += G
-        del G
+
+        def update(Hb, Gb):
+            Gb *= 2.0 / (n + m)
+            Hb *= n / (n + m)
+            Hb += Gb
+
+        if not wide:
+            update(H, _xtx(Xd))
+        for j in _blocks(cols) if wide else ():
+            Gj, Hj = G[j.start:, :j.stop - j.start], H[j.start:, j]
+            np.matmul(Xd[:, j.start:].T, Xd[:, j], out=Gj)
+            _in_threads(lambda r: update(Hj[r], Gj[r]), _blocks(len(Gj)))
         n += m
+    if wide:
+        _mirror(H)
     return H, n
 
 
@@ -141,7 +180,7 @@ def act_order_perm(H: np.ndarray) -> np.ndarray:
 # factorizations run as the textbook block algorithms over WIDE_BLOCK columns, each
 # block step a LAPACK call of order WIDE_BLOCK or a general matrix product.
 LAPACK32_MAX_ORDER = 46340
-WIDE_BLOCK = 8192
+WIDE_BLOCK = 4096
 
 
 def _cholesky_lower_blocked(A: np.ndarray, nb: int = WIDE_BLOCK, overwrite: bool = False):
@@ -189,13 +228,13 @@ def _tri_inverse_lower_blocked(L: np.ndarray, nb: int = WIDE_BLOCK) -> np.ndarra
 
 def _lower_gram_of_lower(X: np.ndarray, nb: int = WIDE_BLOCK) -> np.ndarray:
     """The lower triangle (by block columns; zeros above them) of X^T X for lower
-    triangular X: entry (i, j) sums X[k, i] X[k, j] over k >= j, since X[k, j] = 0
-    for k < j, so block column j0 .. j1-1 takes only rows k >= j0."""
+    triangular X: entry (i, j) with i >= j sums X[k, i] X[k, j] over k >= i, since
+    X[k, i] = 0 for k < i, so block (i, j) takes only the rows from i's first on."""
     n = X.shape[0]
     G = np.zeros((n, n))
-    for j0 in range(0, n, nb):
-        j1 = min(j0 + nb, n)
-        G[j0:, j0:j1] = X[j0:, j0:].T @ X[j0:, j0:j1]
+    for i in _blocks(n, nb):
+        for j in _blocks(i.stop, nb):
+            np.matmul(X[i.start:, i].T, X[i.start:, j], out=G[i, j])
     return G
 
 
@@ -209,8 +248,14 @@ def _inverse_cholesky_upper_wide(Hp: np.ndarray, nb: int = WIDE_BLOCK) -> np.nda
     Hinv = _lower_gram_of_lower(Linv, nb)
     del Linv
     Lu = _cholesky_lower_blocked(Hinv, nb, overwrite=True)
-    U = np.ascontiguousarray(Lu.T)
-    del Lu, Hinv
+    del Hinv
+    U = np.empty_like(Lu)
+
+    def rows(i):
+        for j in _blocks(len(U)):
+            U[i, j] = Lu[j, i].T
+
+    _in_threads(rows, _blocks(len(U)))
     return U
 
 
