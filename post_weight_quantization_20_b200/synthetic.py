@@ -62,9 +62,17 @@ def to_storage(a32: np.ndarray, dtype: str) -> np.ndarray:
 
 def to_f64(a: np.ndarray, dtype: str) -> np.ndarray:
     """Exact widening of a storage array to float64."""
-    if dtype == BF16:
-        return bf16_bits_to_f32(a).astype(np.float64)
-    return np.asarray(a).astype(np.float64)
+    a = np.asarray(a)
+    if a.size < 1 << 24:
+        return (bf16_bits_to_f32(a) if dtype == BF16 else a).astype(np.float64)
+    out = np.empty(a.shape)
+    rows = max(1, len(a) // 64)
+
+    def work(r):
+        out[r:r + rows] = bf16_bits_to_f32(a[r:r + rows]) if dtype == BF16 else a[r:r + rows]
+
+    _pool_map(work, range(0, len(a), rows), _threads())
+    return out
 
 
 def to_f32(a: np.ndarray, dtype: str) -> np.ndarray:
@@ -85,10 +93,16 @@ def _student_t4(g: np.random.Generator, n: int) -> np.ndarray:
     """Student-t with 4 degrees of freedom: Z / sqrt(V/4), V ~ chi^2_4 = -2 ln(U1 U2)."""
     z = g.standard_normal(n, dtype=np.float32)
     u = g.random(2 * n, dtype=np.float32)
-    # (0, 1] keeps the log finite
-    u = np.float32(1.0) - u
-    v = -2.0 * np.log(u[:n] * u[n:])
-    return (z / np.sqrt(v * np.float32(0.25))).astype(np.float32)
+    # (0, 1] keeps the log finite; everything in place, for these arrays are large
+    np.subtract(np.float32(1.0), u, out=u)
+    v = u[:n]
+    v *= u[n:]
+    np.log(v, out=v)
+    v *= np.float32(-2.0)
+    v *= np.float32(0.25)
+    np.sqrt(v, out=v)
+    z /= v
+    return z
 
 
 def _pool_map(fn, items, threads):
