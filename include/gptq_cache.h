@@ -67,7 +67,7 @@ typedef struct {
   int64_t pages;
   int64_t page_size;
   int64_t heads;
-  int64_t dim; /* a multiple of 8 */
+  int64_t dim; /* a multiple of 8, at most 4096 */
 } gptq_cache;
 
 /* Which position of which sequence each row of a call is (device pointers). */

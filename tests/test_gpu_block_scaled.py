@@ -74,6 +74,34 @@ def test_quantize_is_the_definition_bit_for_bit(R, C, pad, dtype):
         assert (out.t[:, C:] == 7.0).all()
 
 
+@pytest.mark.parametrize("R,C,ld", [(9, 1100, 1101), (9, 515, 517), (140, 700, 703), (9, 2049, 2055),
+                                    (9, 129, 131), (9, 513, 513), (9, 4096, 4097)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_at_every_offset_from_16_bytes(R, C, ld, dtype):
+    # ld is odd, so nine rows start at each multiple of the element size from a 16-byte boundary;
+    # the buffer itself starts at an odd element.  What lies between rows is not read or written
+    t, x = _values(R, C, dtype, R + C)
+    c, e = L.mx_quantize(x)
+
+    def view(flat):
+        return flat[1:1 + R * ld].view(R, ld)[:, :C]
+
+    flat = torch.full((R * ld + 1,), float("nan"), dtype=dtype, device=DEV)
+    view(flat).copy_(t)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = MX.mx_quantize(view(flat), st)
+    np.testing.assert_array_equal(q.codes.cpu().numpy().view(np.uint32), o.pack(c.astype(np.int64), 4))
+    at = [[L.mx_scale_index(r, k, e.shape[1]) for k in range(e.shape[1])] for r in range(R)]
+    np.testing.assert_array_equal(q.scales.cpu().numpy().ravel()[at], e)
+    assert int(st) == 0
+    for dt in TYPES:
+        out = Guarded((R * ld + 1,), dt, DEV, fill=torch.full((R * ld + 1,), 7.0, dtype=dt))
+        MX.gptq_mx_dequantize(q.codes, q.scales, view(out.t))
+        want = torch.full((R * ld + 1,), 7.0, dtype=dt)
+        view(want).copy_(torch.from_numpy(L.mx_values(c, e)[:, :C]).to(dt))
+        assert torch.equal(out.t.cpu(), want) and out.intact()
+
+
 def test_quantize_edges():
     f = np.float32
     rows = np.zeros((12, 64), dtype=f)

@@ -117,6 +117,78 @@ def test_write_and_read_are_the_definition(conf, heads, dim, dtype):
             assert (got[..., dim:] == 7.0).all() and (got[len(slots):] == 7.0).all()
 
 
+def _check(call, conf, pools, rows, read):
+    """The cache's live slots and what `read` gave hold the definition of the rows (K, V)."""
+    live = call.slots >= 0
+    for x, codes, grids, got in zip(rows, pools[::2], pools[1::2], read):
+        words, g, vals = _define(x.double().cpu().numpy()[live], *conf)
+        c = codes.t.cpu().numpy().reshape(-1, *words.shape[1:])[call.slots[live]]
+        np.testing.assert_array_equal(c.view(np.uint32), words)
+        gr = grids.t.cpu().numpy().reshape(-1, *g.shape[1:])[call.slots[live]]
+        np.testing.assert_array_equal(_bits(gr), _bits(g.astype(gr.dtype)))
+        assert torch.equal(got.cpu()[torch.from_numpy(live)], torch.from_numpy(vals).to(got.dtype))
+    assert all(p.intact() for p in pools)
+
+
+LAYOUTS = {
+    # (rows, heads, dim) views of a buffer of `rows * (heads + 1) * (dim + 8) + 1` elements
+    "off 16 bytes": lambda b, n, h, d: b[1:1 + n * h * d].view(n, h, d),
+    "odd rows": lambda b, n, h, d: b[:n * (h * d + 1)].view(n, h * d + 1)[:, :h * d].unflatten(1, (h, d)),
+    "head-major": lambda b, n, h, d: b[:n * h * d].view(h, n, d).transpose(0, 1),
+    "head-major, padded, off 16 bytes":
+        lambda b, n, h, d: b[1:1 + n * h * (d + 1)].view(h, n, d + 1)[..., :d].transpose(0, 1),
+}
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("conf", [CONFIGS[1], CONFIGS[2], CONFIGS[4], CONFIGS[7]], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("heads,dim", [(3, 80), (8, 128)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_of_other_alignments_and_orders(layout, conf, heads, dim, dtype):
+    # values and keys of layouts of their own, written from one and read into the other
+    call = Call([1, 30, 9], [3, 0, 20], 16, seed=dim)
+    n, cfg = call.rows, KV.make_cache_config(*conf)
+    size = n * (heads + 1) * (dim + 8) + 1
+
+    def views(dt, swap):
+        a, b = (Guarded((size,), dt, DEV, fill=torch.full((size,), 7.0, dtype=dt)) for _ in range(2))
+        odd, even = LAYOUTS[layout](a.t, n, heads, dim), b.t[:n * heads * dim].view(n, heads, dim)
+        return (a, b), ((even, odd) if swap else (odd, even))
+
+    _, (K, V) = views(dtype, False)
+    K.copy_(_input(n, heads, dim, dtype, 1))
+    V.copy_(_input(n, heads, dim, dtype, 2))
+    pools = _pools(cfg, call, heads, dim)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    KV.gptq_cache_write(K, V, cfg, *(p.t for p in pools), *call.args(), st)
+    for swap in (False, True):
+        bufs, out = views(dtype, swap)
+        KV.gptq_cache_read(cfg, *(p.t for p in pools), *call.args(), *out, st)
+        _check(call, conf, pools, (K, V), out)
+        # nothing beside the rows is written
+        for t in out:
+            t.fill_(7.0)
+        assert all(b.intact() and (b.t == 7.0).all() for b in bufs)
+    assert int(st) == 0
+
+
+@pytest.mark.parametrize("conf", CONFIGS[1:4] + CONFIGS[6:], ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("heads,dim", [(2, 264), (3, 512), (1, 4096), (5, 1000)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_wide_heads(conf, heads, dim, dtype):
+    # up to the largest head; a row of more lanes than a CTA among them
+    call = Call([1, 0, 18], [3, 0, 20], 16, seed=dim)
+    n, cfg = call.rows, KV.make_cache_config(*conf)
+    K, V = (_input(n, heads, dim, dtype, i).to(DEV) for i in range(2))
+    pools = _pools(cfg, call, heads, dim)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    KV.gptq_cache_write(K, V, cfg, *(p.t for p in pools), *call.args(), st)
+    out = torch.zeros_like(K), torch.zeros_like(V)
+    KV.gptq_cache_read(cfg, *(p.t for p in pools), *call.args(), *out, st)
+    _check(call, conf, pools, (K, V), out)
+    assert int(st) == 0
+
+
 @pytest.mark.parametrize("page", [1, 7, 24, 128])
 @pytest.mark.parametrize("conf", [CONFIGS[1], CONFIGS[4], CONFIGS[7]], ids=lambda c: "-".join(map(str, c)))
 def test_rows_one_by_one_equal_a_whole_prompt(conf, page):
