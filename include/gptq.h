@@ -256,8 +256,8 @@ gptq_status gptq_dequant_matmul(const void* X, int xdtype, int64_t m_tokens, int
 gptq_status gptq_selftest_timeout(int which, int32_t* dev_status, void* stream);
 
 /* Diagnostic (the pages have no counterpart): the number of polls after which a
- * wait in the tensor-core pipelines (the Hessian and the 3xTF32 products) gives up,
- * for kernels launched after this call; 0 restores the default (about a second).
+ * wait in the tensor-core pipelines (the Hessian, the 3xTF32 and the 4-bit products)
+ * gives up, for kernels launched after this call; 0 restores the default (about a second).
  * With a small value the waits run out during normal work, so that a test can
  * check that such a kernel stops its producer and MMA issuer, waits for the copies
  * and MMAs it has in flight (those waits keep the default limit), frees its TMEM,

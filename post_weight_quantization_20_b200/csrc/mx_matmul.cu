@@ -240,7 +240,10 @@ k_mx_few(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUten
         if (row + i < p.R) y[i] = from_f32<T>(o[i]);
     }
     __syncwarp();
-    tc::cluster_sync_relaxed();        // no CTA leaves while its partial sums are read
+    // No CTA leaves while its partial sums are read.  An execution barrier is enough: the first
+    // lane of a warp has a layer row (r0 < R) and stores what the whole warp's load brought, so
+    // every load has arrived before its warp does.
+    tc::cluster_sync_relaxed();
   }
   if (*abort_flag) {
     if (warp == 0 && lane == 0) tc::drain_tma_ring(full, C::STAGES, issued);
@@ -637,8 +640,10 @@ bool encode_scales(CUtensorMap* m, const uint8_t* scales, uint64_t ct, uint64_t 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of CTAs that fill an SM each that run at once: SMs come in groups whose size is no
-// multiple of 4 or 8 (148 SMs: 74 clusters of 2, 33 of 4, 15 of 8 by the occupancy query).
+// Clusters of CTAs that fill an SM each that run at once, to choose a split of K by: SMs come in
+// groups whose size is no multiple of 4 or 8.  A share of the SMs, just below what the occupancy
+// query gives (of 148 SMs 74, 32 and 14 clusters of 2, 4 and 8 for 74, 33 and 15): a split that
+// is one cluster too many costs a second wave, one that is not taken some of its gain.
 int64_t clusters_at_once(int ctas, int sms) {
   return ctas <= 2 ? sms / ctas : ctas <= 4 ? sms * 2 / 9 : sms / 10;
 }
@@ -704,7 +709,8 @@ gptq_status by_tokens(cudaStream_t st, const uint32_t* xc, const uint32_t* wc, u
   // K split over clusters where there are few tokens or few layer rows.  Measured (few tokens'
   // kernel against pairs, us): 16 tokens 4096 x 11008 6.4 / 11.9, 49152 x 12288 55.7 / 53.9; 64
   // tokens 4096 x 11008 7.9 / 12.2, 5120 x 5120 7.7 / 7.8, 11008 x 4096 8.3 / 7.2, 49152 x 12288
-  // 64.9 / 54.0; 128 tokens 12288 x 12288 21.7 / 14.2.
+  // 64.9 / 54.0; 128 tokens 12288 x 12288 21.7 / 14.2.  Up to 32 tokens the pairs, whose least
+  // tile is 64 of them, win on the widest layers only, by 3%: there the rule has no exception.
   p.ntr = (p.R + 255) / 256;
   if (p.M <= 16) return launch_few<16, T>(st, xc, wc, row_bytes, p, sms, status);
   if (p.M <= 32) return launch_few<32, T>(st, xc, wc, row_bytes, p, sms, status);
